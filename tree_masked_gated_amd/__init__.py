@@ -1,7 +1,7 @@
 """Python binding of libgdntree.so: rollback-free GDN draft-tree verification on
 MI355X (gfx950).
 
-The names mirror the C ABI in include/gdn_tree.h.  This module only marshals
+The names mirror the C ABI in include/gdn_tree.h and include/gdn_attn.h.  This module only marshals
 arguments: it checks that each torch tensor has the shape, dtype and
 contiguity the C ABI documents (so a kernel never reads past a buffer) and
 passes device pointers and the current HIP stream.  Every step of the
@@ -11,6 +11,7 @@ provides device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Dict, Optional
 
@@ -21,6 +22,10 @@ __all__ = [
     "gdn_tree_commit_verify_ragged", "gdn_tree_accept_ragged", "check_offsets",
     "BuildDims", "build_dims", "gdn_tree_build",
     "gdn_tree_strerror", "TreeCache",
+    "ROPE_HALF", "ROPE_INTERLEAVED", "AttnDims", "RopeDims", "PageDims", "AttnRows", "PagedCacheStruct",
+    "PagedCache", "attn_dims", "rope_dims", "page_dims", "attn_workspace", "gdn_attn_workspace_bytes",
+    "gdn_attn_rope", "gdn_attn_verify", "gdn_attn_commit", "gdn_pages_fork", "gdn_pages_reserve",
+    "gdn_pages_copy", "gdn_pages_free", "gdn_pages_compact",
 ]
 
 GDN_F32, GDN_BF16 = 0, 1
@@ -443,3 +448,249 @@ def _check_cache(c: TreeCache, d: Dims):
     cd = c.dims
     if (cd.batch, cd.n_nodes, cd.h_v, cd.d_v) != (d.batch, d.n_nodes, d.h_v, d.d_v):
         raise ValueError("cache was allocated for different dims")
+
+
+# ---------------------------------------------------------------- attention layers
+# Softmax attention of the same trees (include/gdn_attn.h): rotary positions, attention
+# over a paged cache, append of the accepted path, page bookkeeping.  Tensors of rows
+# ([T, heads, d]) may be strided slices; a ragged call takes `offsets`.
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "n_nodes", "h_q", "h_kv", "d", "io_dtype")] + \
+        [("scale", ctypes.c_float)]
+
+
+class RopeDims(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("amp", ctypes.c_double)]
+
+
+class PageDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_pages", "page_rows", "n_slots", "width")]
+
+
+class AttnRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + \
+        [(n, ctypes.c_int32) for n in ("n_layers", "n_pages", "page_rows", "h_kv", "d", "io_dtype")] + \
+        [(n, ctypes.c_int64) for n in ("k_layer", "k_page", "k_row", "k_head",
+                                       "v_layer", "v_page", "v_row", "v_head")]
+
+
+_ar, _i32, _i64 = ctypes.POINTER(AttnRows), ctypes.c_int32, ctypes.c_int64
+_ad, _pd, _pc = ctypes.POINTER(AttnDims), ctypes.POINTER(PageDims), ctypes.POINTER(PagedCacheStruct)
+for _name, _args in {
+        "gdn_attn_rope": [_ad, ctypes.POINTER(RopeDims), _vp, _i64, _ar, _ar, _vp, _vp, _vp, _ar, _ar, _vp],
+        "gdn_attn_workspace_bytes": [_ad, _sz],
+        "gdn_attn_verify": [_ad, _vp, _pc, _i32, _vp, _i32, _vp, _ar, _ar, _ar, _vp, _vp, _ar, _vp, _vp],
+        "gdn_attn_commit": [_ad, _vp, _pc, _i32, _vp, _i32, _vp, _ar, _ar, _vp, _vp, _vp, _vp],
+        "gdn_pages_fork": [_pd, _i32] + [_vp] * 8,
+        "gdn_pages_reserve": [_pd] + [_vp] * 10,
+        "gdn_pages_copy": [_pc, _i32] + [_vp] * 4,
+        "gdn_pages_free": [_pd] + [_vp] * 6,
+        "gdn_pages_compact": [_pd, _i32] + [_vp] * 8}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _i
+
+
+def attn_dims(batch, n_nodes, h_q, h_kv, d, io_dtype, scale=None) -> AttnDims:
+    """scale: the factor of q.k, d ** -0.5 unless given."""
+    if isinstance(io_dtype, str):
+        io_dtype = {"f32": GDN_F32, "bf16": GDN_BF16}[io_dtype]
+    return AttnDims(batch, n_nodes, h_q, h_kv, d, io_dtype, d ** -0.5 if scale is None else scale)
+
+
+def rope_dims(rot, layout="half", amp=1.0) -> RopeDims:
+    if isinstance(layout, str):
+        layout = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}[layout]
+    return RopeDims(rot, layout, amp)
+
+
+def page_dims(n_pages, page_rows, n_slots, width) -> PageDims:
+    return PageDims(n_pages, page_rows, n_slots, width)
+
+
+class PagedCache:
+    """Key and value pools as one gdn_paged_cache: tensors [pages, page_rows, h_kv, d], or
+    with a leading axis of layers, of any strides with the last axis contiguous (a pool kept
+    heads first is passed as its transposed view)."""
+
+    def __init__(self, k, v):
+        torch = _torch()
+        if k.shape != v.shape or k.dtype != v.dtype or k.dim() not in (4, 5):
+            raise ValueError("PagedCache: k and v [layers,] pages, page_rows, h_kv, d of one shape and dtype")
+        if k.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"PagedCache: dtype {k.dtype}")
+        if not (k.is_cuda and v.is_cuda):
+            raise ValueError("PagedCache: must be device tensors")
+        if k.stride(-1) != 1 or v.stride(-1) != 1:
+            raise ValueError("PagedCache: the last axis must be contiguous")
+        self.k, self.v = k, v
+        pages, rows, heads, d = k.shape[-4:]
+        lead = lambda t: (t.stride(0) if t.dim() == 5 else 0, *t.stride()[-4:-1])  # noqa: E731
+        self.struct = PagedCacheStruct(
+            k.data_ptr(), v.data_ptr(), k.shape[0] if k.dim() == 5 else 1, pages, rows, heads, d,
+            GDN_F32 if k.dtype == torch.float32 else GDN_BF16, *lead(k), *lead(v))
+
+
+def _cache_ref(cache):
+    if isinstance(cache, PagedCache):
+        return ctypes.byref(cache.struct)
+    if isinstance(cache, PagedCacheStruct):
+        return ctypes.byref(cache)
+    raise TypeError("cache: expected PagedCache or PagedCacheStruct")
+
+
+def _attn_rows(x, rows, heads, d, io, name):
+    """gdn_attn_rows of a [rows, heads, d] tensor with a contiguous last axis."""
+    if x.dtype != io or not x.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor of {io}")
+    if x.shape != (rows, heads, d):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(rows, heads, d)}")
+    row, head, one = x.stride()
+    if one != 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    return AttnRows(x.data_ptr(), row, head)
+
+
+def _ints(x, shape, name):
+    """Device pointer of a contiguous int32 tensor of this shape."""
+    torch = _torch()
+    if x.dtype != torch.int32 or not x.is_cuda or not x.is_contiguous() or x.shape != shape:
+        raise ValueError(f"{name}: expected a contiguous int32 device tensor of shape {tuple(shape)}, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+    return x.data_ptr()
+
+
+def _attn_offsets(offsets, d, x):
+    """Offsets pointer and number of rows of a dense or ragged call whose first row tensor is x."""
+    if offsets is None:
+        return None, d.batch * d.n_nodes
+    return _ints(offsets, (d.batch + 1,), "offsets"), x.shape[0]
+
+
+def _call(fn, *args):
+    rc = getattr(_lib, fn)(*args)
+    if rc:
+        raise GdnError(rc, fn)
+
+
+def gdn_attn_rope(d: AttnDims, rope: RopeDims, q, k, freq, ctx, depth, q_out, k_out, offsets=None,
+                  stream=None) -> None:
+    """Enqueue the rotation of the trees' queries and keys to their nodes' positions (see
+    gdn_attn.h).  freq: float64 [rot / 2]; depth: [B, N], TreeCache.depth."""
+    torch = _torch()
+    io = _io_dtype(d)
+    off, T = _attn_offsets(offsets, d, q)
+    if freq.dtype != torch.float64 or freq.shape != (rope.rot // 2,) or not freq.is_cuda or not freq.is_contiguous():
+        raise ValueError(f"freq: expected a contiguous float64 device tensor of {rope.rot // 2} values")
+    _call("gdn_attn_rope", ctypes.byref(d), ctypes.byref(rope), off, T,
+          _attn_rows(q, T, d.h_q, d.d, io, "q"), _attn_rows(k, T, d.h_kv, d.d, io, "k"), freq.data_ptr(),
+          _ints(ctx, (d.batch,), "ctx"), _ints(depth, (d.batch, d.n_nodes), "depth"),
+          _attn_rows(q_out, T, d.h_q, d.d, io, "q_out"), _attn_rows(k_out, T, d.h_kv, d.d, io, "k_out"),
+          _stream(stream))
+
+
+def gdn_attn_workspace_bytes(d: AttnDims) -> int:
+    out = ctypes.c_size_t()
+    _call("gdn_attn_workspace_bytes", ctypes.byref(d), ctypes.byref(out))
+    return out.value
+
+
+def attn_workspace(d: AttnDims, device="cuda"):
+    """A zeroed workspace for gdn_attn_verify calls of these dims, one after the other."""
+    torch = _torch()
+    return torch.zeros(max(gdn_attn_workspace_bytes(d), 16), dtype=torch.uint8, device=device)
+
+
+def gdn_attn_verify(d: AttnDims, cache, table, ctx, q, k, v, anc_mask, tree_status, o, workspace,
+                    offsets=None, layer=0, stream=None) -> None:
+    """Enqueue the attention of every node of every tree over its sequence's pages, its
+    ancestors and itself (see gdn_attn.h).  anc_mask and tree_status: TreeCache's."""
+    torch = _torch()
+    B, N, io = d.batch, d.n_nodes, _io_dtype(d)
+    off, T = _attn_offsets(offsets, d, q)
+    if table.dim() != 2:
+        raise ValueError("table: expected [B, width]")
+    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() or \
+            workspace.numel() < _workspace_bytes(d):
+        raise ValueError(f"workspace: expected {_workspace_bytes(d)} contiguous bytes (attn_workspace)")
+    _call("gdn_attn_verify", ctypes.byref(d), off, _cache_ref(cache), layer,
+          _ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
+          _attn_rows(q, T, d.h_q, d.d, io, "q"), _attn_rows(k, T, d.h_kv, d.d, io, "k"),
+          _attn_rows(v, T, d.h_kv, d.d, io, "v"), _ints(anc_mask, (B, N, (N + 31) // 32), "anc_mask"),
+          _ints(tree_status, (B,), "tree_status"), _attn_rows(o, T, d.h_q, d.d, io, "o"),
+          workspace.data_ptr(), _stream(stream))
+
+
+@functools.lru_cache(maxsize=None)
+def _workspace_bytes_of(*sizes):
+    return gdn_attn_workspace_bytes(AttnDims(*sizes, 1.0))
+
+
+def _workspace_bytes(d: AttnDims) -> int:
+    return _workspace_bytes_of(d.batch, d.n_nodes, d.h_q, d.h_kv, d.d, d.io_dtype)
+
+
+def gdn_attn_commit(d: AttnDims, cache, table, ctx, k, v, path, path_len, new_len, offsets=None, layer=0,
+                    stream=None) -> None:
+    """Enqueue the append of the accepted paths' keys and values to the cache (see gdn_attn.h).
+    path, path_len: as gdn_tree_commit (ragged: gdn_tree_commit_ragged) writes them."""
+    B, io = d.batch, _io_dtype(d)
+    off, T = _attn_offsets(offsets, d, k)
+    if table.dim() != 2:
+        raise ValueError("table: expected [B, width]")
+    _call("gdn_attn_commit", ctypes.byref(d), off, _cache_ref(cache), layer,
+          _ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
+          _attn_rows(k, T, d.h_kv, d.d, io, "k"), _attn_rows(v, T, d.h_kv, d.d, io, "v"),
+          _ints(path, (B, d.n_nodes) if offsets is None else (T,), "path"),
+          _ints(path_len, (B,), "path_len"), _ints(new_len, (B,), "new_len"), _stream(stream))
+
+
+def _page_state(pd, ref, table, held, length):
+    return (_ints(ref, (pd.n_pages,), "ref"), _ints(table, (pd.n_slots, pd.width), "table"),
+            _ints(held, (pd.n_slots,), "held"), _ints(length, (pd.n_slots,), "length"))
+
+
+def gdn_pages_fork(pd: PageDims, src_seq, dst_seq, ref, table, held, length, status, stream=None) -> None:
+    """Enqueue dst_seq[i] becoming a second holder of src_seq[i]'s pages (see gdn_attn.h)."""
+    n = src_seq.numel()
+    _call("gdn_pages_fork", ctypes.byref(pd), n, _ints(src_seq, (n,), "src_seq"), _ints(dst_seq, (n,), "dst_seq"),
+          *_page_state(pd, ref, table, held, length), _ints(status, (n,), "status"), _stream(stream))
+
+
+def gdn_pages_reserve(pd: PageDims, need, ref, table, held, length, src, dst, count, status, stream=None) -> None:
+    """Enqueue the allocation of need[s] more rows per sequence (see gdn_attn.h); the page copies it
+    takes are src, dst, count, for gdn_pages_copy."""
+    S = pd.n_slots
+    _call("gdn_pages_reserve", ctypes.byref(pd), _ints(need, (S,), "need"),
+          *_page_state(pd, ref, table, held, length), _ints(src, (S,), "src"), _ints(dst, (S,), "dst"),
+          _ints(count, (1,), "count"), _ints(status, (S,), "status"), _stream(stream))
+
+
+def gdn_pages_copy(cache, src, dst, count, stream=None) -> None:
+    """Enqueue the copies of pages src[i] to dst[i], i < count, in every layer (see gdn_attn.h)."""
+    n = src.numel()
+    _call("gdn_pages_copy", _cache_ref(cache), n, _ints(src, (n,), "src"), _ints(dst, (n,), "dst"),
+          _ints(count, (1,), "count"), _stream(stream))
+
+
+def gdn_pages_free(pd: PageDims, drop, ref, table, held, length, stream=None) -> None:
+    """Enqueue the return of the pages of every sequence with drop[s] != 0 (see gdn_attn.h)."""
+    _call("gdn_pages_free", ctypes.byref(pd), _ints(drop, (pd.n_slots,), "drop"),
+          *_page_state(pd, ref, table, held, length), _stream(stream))
+
+
+def gdn_pages_compact(pd: PageDims, ref, table, held, src, dst, count, remap, stream=None) -> None:
+    """Enqueue the move of held pages to the front of the pool: bookkeeping here, data by
+    gdn_pages_copy(cache, src, dst, count).  At most src.numel() pages move."""
+    n = src.numel()
+    _call("gdn_pages_compact", ctypes.byref(pd), n, _ints(ref, (pd.n_pages,), "ref"),
+          _ints(table, (pd.n_slots, pd.width), "table"), _ints(held, (pd.n_slots,), "held"),
+          _ints(src, (n,), "src"), _ints(dst, (n,), "dst"), _ints(count, (1,), "count"),
+          _ints(remap, (pd.n_pages,), "remap"), _stream(stream))

@@ -20,7 +20,9 @@ LIB = os.path.join(HERE, "libgdntree.so")
 OBJDIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["abi.hip", "verify_generic.hip", "verify_tiled.hip", "verify_large.hip", "commit.hip", "build.hip",
-           "accept.hip"]
+           "accept.hip", "attn_abi.hip", "attn_rope.hip", "attn_pages.hip",
+           "attn_verify_bf16_64.hip", "attn_verify_bf16_128.hip", "attn_verify_bf16_256.hip",
+           "attn_verify_f32_64.hip", "attn_verify_f32_128.hip", "attn_verify_f32_256.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", f"-I{INCLUDE}",
@@ -41,7 +43,7 @@ def _compile(src: str) -> str:
     return obj
 
 
-def build(jobs: int = 4) -> str:
+def build(jobs: int = 8) -> str:
     """Compile every source and link libgdntree.so; returns its path."""
     os.makedirs(OBJDIR, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]

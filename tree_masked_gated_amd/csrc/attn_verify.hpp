@@ -1,0 +1,895 @@
+// attn_verify.hpp -- attention of a draft tree over a paged cache: the kernel, as a
+// template on element type, head size and the shape of its tiles.
+//
+// Mathematics.  The rows of one (sequence, key head) are the n nodes times the group of
+// query heads that share the key head.  All of them see the prefix; node i also sees its
+// strict ancestors and itself.  The keys of a sequence are one run of ctx + n rows, the
+// prefix through the page table, then the tree's own rows; only tiles that reach past ctx
+// look at the ancestor bits.  One pass over the keys with a running maximum m (in powers of
+// two, scores times scale log2 e), sum l and output acc per row:
+//     p = 2^(s - m),  l += p,  acc += p v,
+// and where m grows, l and acc are first multiplied by 2^(m_old - m_new).  m may lag behind
+// the true maximum by up to kLag: the quotient acc / l does not depend on it, p stays below
+// 2^kLag, and most tiles then skip the multiplication.
+//
+// Tiles.  Scores are formed transposed, S^T = K Q^T, with 16 x 16 matrix instructions: a
+// lane then holds four keys of one row, the row's statistics are the lane's own, and the
+// packed weights are the second operand of O^T = V^T P^T as they are, provided that V's
+// operand lists its keys in the same order.  For bf16 that operand is read from LDS by the
+// transposing 64-bit read (four keys of one column per lane); for fp32 its elements are
+// single words.  The 16-byte pieces of a key's row are stored at piece c ^ swizzle(key), which
+// spreads both the rows of K (same piece, 16 keys) and the columns of V (four keys, four
+// pieces) over all banks.
+//
+// Work.  Tiles of all (sequence, key head, block of rows) form one line, cut into equal
+// shares, one per workgroup, so that contexts of very different lengths keep all CUs busy
+// to the end without the host knowing the lengths.  A block of rows whose keys were cut
+// leaves partial results (m, l, acc in fp32) in the workspace; the workgroup that arrives
+// last, by a counter, joins them in the order of the keys, so that results do not depend
+// on the order of arrival.
+#pragma once
+
+#include "attn_common.hpp"
+
+namespace gdn {
+namespace attn {
+
+constexpr int kCUs = 256, kXcds = 8;
+constexpr int kThreads = 256;
+constexpr int kMaxCtx = 0x7fff0000;          // key indexes, whole tiles of them, are 32 bits
+constexpr float kLag = 8.0f;
+constexpr int kMaxParts = 64;                // pieces of one block of rows
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// IO, D: element type and head size (padded with zeros); RT: tiles of 16 rows per wave;
+// WR: waves side by side over rows, WK = 4 / WR over keys; KT: keys per wave and step.
+template <int IO_, int D_, int RT_, int WR_, int KT_, int OCC_>
+struct Cfg {
+    static constexpr int IO = IO_, D = D_, RT = RT_, WR = WR_, KT = KT_, OCC = OCC_;
+    static constexpr int WK = 4 / WR;
+    static constexpr int ES = IO == GDN_F32 ? 4 : 2;
+    static constexpr int E = 16 / ES;                   // elements of a 16-byte piece
+    static constexpr int CPR = D / E;                   // pieces of a row
+    static constexpr int BM = RT * 16 * WR;             // rows of a workgroup
+    static constexpr int KW = KT * WK;                  // keys of a workgroup's step
+    static constexpr int TG = 64 * WR;                  // threads that share keys
+    static constexpr int NCH = KT * CPR / TG;           // pieces of K (and of V) per thread and step
+    static constexpr int KSTEP = TG / CPR;              // keys between a thread's pieces
+    static constexpr int STAGES = WR == 1 ? 1 : 2;
+    static constexpr int ROWB = D * ES;
+    static constexpr int TILEB = KT * ROWB;
+    static constexpr int LDS = STAGES * WK * 2 * TILEB;
+    static constexpr int DT = D / 16;                   // tiles of 16 columns
+    static constexpr int DQ = DT / WK;                  // of these, a wave's share at the end
+    static constexpr int KTILES = KT / 16;
+    static constexpr int SLOT = BM * (D + 2) * 4;       // bytes of a partial result
+    static_assert(LDS + 4096 <= kMaxLds, "LDS of a workgroup");
+    static_assert(TG % CPR == 0 && NCH >= 1, "a thread keeps its piece of the row");
+    static_assert(KT % 32 == 0 && KT <= 64, "mask words");
+};
+
+// Launch parameters that depend on the configuration.
+struct Plan {
+    int grid;          // workgroups
+    int side;          // C: workgroups that take neighbouring blocks of rows over the same keys
+    int clusters;      // grid / C
+    int max_blocks;    // blocks of rows of the largest tree
+    int32_t* arrived;  // [B][Hk][max_blocks]
+    char* slots;       // [grid][2][SLOT]
+};
+
+template <class C>
+__device__ __forceinline__ int swizzle(int key) {
+    if constexpr (C::IO == GDN_F32)
+        return (((key >> 2) & 3) << 2) | (key & 3);
+    else if constexpr (C::CPR == 8)
+        return (((key >> 1) & 1) << 2) | ((key >> 2) & 3);
+    else
+        return ((key & 3) << 2) | ((key >> 2) & 3);
+}
+
+// Sequence b: its rows, prefix and share of the work.
+struct Seq {
+    int64_t row0;
+    int n, ctx, blocks, tiles, groups;       // groups: ceil(blocks / side)
+    bool poison;                             // its rows are NaN
+};
+
+template <class C>
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int side, int o0, int o1, int b, int ctx, int status) {
+    Seq s;
+    s.row0 = (int64_t)b * a.N;
+    s.n = a.N;
+    if (a.offsets != nullptr) {
+        const int64_t n = (int64_t)o1 - o0;
+        const bool usable = o0 >= 0 && n >= 0 && n <= a.N;
+        s.row0 = usable ? o0 : 0;
+        s.n = usable ? (int)n : 0;
+    }
+    s.poison = status != 0 || ctx < 0 || ctx > kMaxCtx || ctx > (int64_t)a.width * (int64_t)a.page.d;
+    s.ctx = s.poison ? 0 : ctx;
+    s.blocks = (s.n * a.group + C::BM - 1) / C::BM;
+    s.groups = (s.blocks + side - 1) / side;
+    s.tiles = s.n == 0 ? 0 : s.poison ? 1 : (int)(((int64_t)s.ctx + s.n + C::KW - 1) / C::KW);
+    return s;
+}
+
+template <class C>
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int side, int b) {
+    const int o0 = a.offsets ? a.offsets[b] : 0, o1 = a.offsets ? a.offsets[b + 1] : 0;
+    return sequence<C>(a, side, o0, o1, b, a.ctx[b], a.status[b]);
+}
+
+__device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+
+// 2^x, one instruction.
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// Replaces infinities and NaN of a 16-byte piece by zero; whether there were any.
+template <int IO>
+__device__ __forceinline__ bool clean(uint4& u) {
+    uint32_t* w = (uint32_t*)&u;
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (IO == GDN_F32) {
+            const bool x = (w[i] & 0x7f800000u) == 0x7f800000u;
+            w[i] = x ? 0u : w[i];
+            any |= x;
+        } else {
+            const bool lo = (w[i] & 0x7f80u) == 0x7f80u, hi = (w[i] & 0x7f800000u) == 0x7f800000u;
+            w[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+            any |= lo || hi;
+        }
+    }
+    return any;
+}
+
+// A wave's view of one (sequence, key head, block of rows) over a run of key tiles.
+template <class C>
+struct Worker {
+    static constexpr int RT = C::RT, DT = C::DT, KTILES = C::KTILES, NCH = C::NCH, ES = C::ES, E = C::E;
+
+    const AttnArgs& a;
+    char* lds;
+    int* s_flag;                             // [2]: a tile's V holds infinities or NaN
+    int lane, wr, wk, tg;                    // tg: thread within its key group
+    int b, h;
+    Seq s;
+
+    typename std::conditional<C::IO == GDN_F32, f32x4[C::D / 16], bf16x8[C::D / 32]>::type q[RT];
+    f32x4 acc[RT][DT];
+    float m[RT], l[RT];
+    int node[RT];
+    uint4 kreg[NCH], vreg[NCH];
+    int pid[NCH];
+    bool bad;
+
+    __device__ __forceinline__ Worker(const AttnArgs& a_, char* lds_, int* flag) : a(a_), lds(lds_), s_flag(flag) {
+        const int tid = threadIdx.x;
+        lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        wr = wave % C::WR;
+        wk = wave / C::WR;
+        tg = tid - wk * C::TG;
+    }
+
+    __device__ __forceinline__ char* ktile(int stage) const { return lds + (stage * C::WK + wk) * 2 * C::TILEB; }
+    __device__ __forceinline__ char* vtile(int stage) const { return ktile(stage) + C::TILEB; }
+
+    __device__ __forceinline__ void begin(int block) {
+        const int g = lane >> 4;
+        bad = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            m[rt] = -INFINITY;
+            l[rt] = 0.f;
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) acc[rt][dt] = zero4();
+            const int r = row_of(block, rt);
+            const bool real = r < s.n * a.group;
+            const int i = (int)quot(a.group_div, r);
+            node[rt] = real ? i : -1;
+            const char* p = a.q.p + (real ? (s.row0 + i) * a.q.row + (h * a.group + (r - i * a.group)) * a.q.head : 0);
+#pragma unroll
+            for (int ks = 0; ks < C::CPR / 4; ++ks) {
+                const int e = (ks * 4 + g) * E;
+                uint4 u = *(const uint4*)(p + (e < a.d ? e * ES : 0));
+                if (!real || e >= a.d) u = uint4{0, 0, 0, 0};
+                q[rt][ks] = __builtin_bit_cast(typename std::remove_reference<decltype(q[0][0])>::type, u);
+            }
+        }
+    }
+
+    __device__ __forceinline__ int row_of(int block, int rt) const {
+        return block * C::BM + (wr * RT + rt) * 16 + (lane & 15);
+    }
+
+    // First key of this wave's part of tile t.
+    __device__ __forceinline__ int key0(int t) const { return t * C::KW + wk * C::KT; }
+
+    __device__ __forceinline__ void fetch_pages(int t) {
+        const int j0 = key0(t) + tg / C::CPR;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int j = j0 + i * C::KSTEP;
+            pid[i] = 0;
+            if (j < s.ctx) pid[i] = a.table[(int64_t)b * a.width + quot(a.page, j)];
+        }
+    }
+
+    // Loads tile t into registers, through the page ids fetched before.  Every load is made; one
+    // that has no row reads the pool's first row, and store() drops what it brought.
+    __device__ __forceinline__ void load(int t) {
+        const int c = tg % C::CPR;
+        const int j0 = key0(t) + tg / C::CPR;
+        const int64_t in_row = c * E < a.d ? c * 16 : 0;
+        const char* kb = a.kp.p + h * a.kp.head + in_row;
+        const char* vb = a.vp.p + h * a.vp.head + in_row;
+        if (!mixed(t)) {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int j = j0 + i * C::KSTEP;
+                const int r = j - (int)quot(a.page, j) * (int)a.page.d;
+                const bool ok = (uint32_t)pid[i] < (uint32_t)a.n_pages;
+                bad |= !ok;
+                const int64_t id = ok ? pid[i] : 0;
+                kreg[i] = *(const uint4*)(kb + id * a.kp.page + r * a.kp.row);
+                vreg[i] = *(const uint4*)(vb + id * a.vp.page + r * a.vp.row);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                const int j = j0 + i * C::KSTEP;
+                const bool prefix = j < s.ctx, tree = !prefix && j < s.ctx + s.n;
+                const int r = prefix ? j - (int)quot(a.page, j) * (int)a.page.d : 0;
+                const bool ok = !prefix || (uint32_t)pid[i] < (uint32_t)a.n_pages;
+                bad |= !ok;
+                const int64_t id = prefix && ok ? pid[i] : 0;
+                const int64_t tr = s.row0 + (j - s.ctx);
+                const char* kq = kb + id * a.kp.page + r * a.kp.row;
+                const char* vq = vb + id * a.vp.page + r * a.vp.row;
+                const char* kt = a.k.p + h * a.k.head + in_row + tr * a.k.row;
+                const char* vt = a.v.p + h * a.v.head + in_row + tr * a.v.row;
+                kreg[i] = *(const uint4*)(tree ? kt : kq);
+                vreg[i] = *(const uint4*)(tree ? vt : vq);
+            }
+        }
+    }
+
+    // Whether this wave's part of tile t reaches the tree's own keys.
+    __device__ __forceinline__ bool mixed(int t) const { return key0(t) + C::KT > s.ctx; }
+
+    // Registers to LDS.
+    __device__ __forceinline__ void store(int t, int stage) {
+        char* kt = ktile(stage);
+        char* vt = vtile(stage);
+        const int c = tg % C::CPR, k0 = tg / C::CPR;
+        if (mixed(t)) {
+            // A zero weight times an infinity is no zero: what is not finite is kept out of the
+            // product and added to the rows that see it (spread()).
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) {
+                if (key0(t) + k0 + i * C::KSTEP >= s.ctx + s.n) vreg[i] = uint4{0, 0, 0, 0};
+                any |= clean<C::IO>(vreg[i]);
+            }
+            if (any) s_flag[stage * C::WK + wk] = 1;
+        }
+        const bool pad = c * E >= a.d;       // columns past d: the query's are zero, the key's must be finite
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const int key = k0 + i * C::KSTEP;
+            if (pad) kreg[i] = uint4{0, 0, 0, 0};
+            const int at = key * C::ROWB + ((c ^ swizzle<C>(key)) * 16);
+            *(uint4*)(kt + at) = kreg[i];
+            *(uint4*)(vt + at) = vreg[i];
+        }
+    }
+
+    // Bits of the keys of block kb (32 keys from key j0 + 32 kb on) that row rt sees.
+    __device__ __forceinline__ uint32_t seen(int j0, int kb, int rt) const {
+        const int x = j0 + 32 * kb - s.ctx;             // node index of the first key
+        const int w0 = x >> 5, sh = x & 31;
+        const uint32_t lo = seen_word(w0, rt), hi = seen_word(w0 + 1, rt);
+        return sh == 0 ? lo : (lo >> sh) | (hi << (32 - sh));
+    }
+    __device__ __forceinline__ uint32_t seen_word(int w, int rt) const {
+        if (w < 0) return 0xffffffffu;                  // the prefix
+        if (node[rt] < 0 || w * 32 >= s.n) return 0u;
+        uint32_t x = a.anc[((int64_t)b * a.N + node[rt]) * a.words + w];
+        if ((node[rt] >> 5) == w) x |= 1u << (node[rt] & 31);
+        const int left = s.n - w * 32;
+        return left < 32 ? x & ((1u << left) - 1u) : x;
+    }
+
+    __device__ __forceinline__ void compute(int t, int stage) {
+        const int g = lane >> 4, c16 = lane & 15;
+        const char* kt = ktile(stage);
+        const char* vt = vtile(stage);
+        f32x4 sc[RT][KTILES];
+#pragma unroll
+        for (int x = 0; x < KTILES; ++x) {
+            const char* row = kt + c16 * C::ROWB + x * 16 * C::ROWB;
+            const int z = swizzle<C>(c16);              // of key 16 x + c16: its low four bits count
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) sc[rt][x] = zero4();
+#pragma unroll
+            for (int ks = 0; ks < C::CPR / 4; ++ks) {
+                const uint4 u = *(const uint4*)(row + ((ks * 4 + g) ^ z) * 16);
+                if constexpr (C::IO == GDN_F32) {
+                    const f32x4 kf = __builtin_bit_cast(f32x4, u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            sc[rt][x] = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[e], q[rt][ks][e], sc[rt][x], 0, 0, 0);
+                } else {
+                    const bf16x8 kf = __builtin_bit_cast(bf16x8, u);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        sc[rt][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[rt][ks], sc[rt][x], 0, 0, 0);
+                }
+            }
+        }
+        const int j0 = key0(t);
+        const bool masked = mixed(t);
+        if (masked) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int kb = 0; kb < C::KT / 32; ++kb) {
+                    const uint32_t bits = seen(j0, kb, rt) >> (4 * g);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((bits >> (16 * x + i)) & 1u)) sc[rt][2 * kb + x][i] = -INFINITY;
+                }
+            }
+        }
+        // running maximum, moved only where it lags too far
+        const float scale = a.scale * kLog2e;
+        float top[RT];
+        bool move = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < KTILES; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[rt] = fmaxf(top[rt], sc[rt][x][i]);
+            top[rt] *= scale;
+            move |= top[rt] > m[rt] + kLag;
+        }
+        if (__any(move)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float x = top[rt];
+                x = fmaxf(x, __shfl_xor(x, 16));
+                x = fmaxf(x, __shfl_xor(x, 32));
+                x = fmaxf(x, m[rt]);
+                const float f = x == m[rt] ? 1.f : exp2_fast(m[rt] - x);
+                m[rt] = x;
+                l[rt] *= f;
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= f;
+            }
+        }
+        typename std::conditional<C::IO == GDN_F32, f32x4, bf16x8>::type p[RT][C::IO == GDN_F32 ? KTILES : KTILES / 2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const float base = m[rt] == -INFINITY ? 0.f : m[rt];
+#pragma unroll
+            for (int x = 0; x < KTILES; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[rt][x][i] = exp2_fast(fmaf(sc[rt][x][i], scale, -base));
+            if constexpr (C::IO == GDN_F32) {
+#pragma unroll
+                for (int x = 0; x < KTILES; ++x) {
+                    p[rt][x] = sc[rt][x];
+                    l[rt] += (sc[rt][x][0] + sc[rt][x][1]) + (sc[rt][x][2] + sc[rt][x][3]);
+                }
+            } else {
+                // The weights are rounded to bf16, 2^-9 of each: the product needs two bf16
+                // operands.  l sums the rounded ones, so that the weights' quotients add up to one
+                // and a row that sees one key gets that key's value exactly.
+                const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+                for (int x = 0; x < KTILES / 2; ++x) {
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const f32x4& src = sc[rt][2 * x + (i >> 2)];
+                        bf16x2 v;
+                        v[0] = (__bf16)src[i & 3];
+                        v[1] = (__bf16)src[(i & 3) + 1];
+                        l[rt] = __builtin_amdgcn_fdot2_f32_bf16(v, one, l[rt], false);
+                        p[rt][x][i] = v[0];
+                        p[rt][x][i + 1] = v[1];
+                    }
+                }
+            }
+        }
+        if constexpr (C::IO == GDN_F32) {
+#pragma unroll
+            for (int x = 0; x < KTILES; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const char* row = vt + 4 * g * C::ROWB + (x * 16 + i) * C::ROWB;
+                    const int z = swizzle<C>(4 * g + i);
+#pragma unroll
+                    for (int dt = 0; dt < DT; ++dt) {
+                        const float v = *(const float*)(row + ((dt * 4 + (c16 >> 2)) ^ z) * 16 + (c16 & 3) * 4);
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            acc[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, p[rt][x][i], acc[rt][dt], 0, 0, 0);
+                    }
+                }
+        } else {
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+#pragma unroll
+            for (int x = 0; x < KTILES / 2; ++x) {
+                // lane (row of the read c16 / 4, columns 4 (c16 % 4) ..): keys 4g + c16 / 4 of both halves
+                const int key = 4 * g + (c16 >> 2);
+                const char* row = vt + key * C::ROWB + (c16 & 1) * 8 + x * 32 * C::ROWB;
+                const int z = swizzle<C>(key);
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    const int c = dt * 2 + ((c16 >> 1) & 1);
+                    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(row + (c ^ z) * 16));
+                    const s16x4 hi =
+                        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(row + 16 * C::ROWB + (c ^ z) * 16));
+                    bf16x8 v;
+                    const bf16x4 vl = __builtin_bit_cast(bf16x4, lo), vh = __builtin_bit_cast(bf16x4, hi);
+                    v = __builtin_shufflevector(vl, vh, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+                        acc[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][x], acc[rt][dt], 0, 0, 0);
+                }
+            }
+        }
+        if (masked && s_flag[stage * C::WK + wk] != 0) spread(j0);
+    }
+
+    // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
+    // key after the other, a few registers, so that it costs the main loop none).
+    __device__ __forceinline__ void spread(int j0) {
+        const int g = lane >> 4;
+#pragma unroll 1
+        for (int kb = 0; kb < C::KT / 32; ++kb) {
+            uint32_t bits[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) bits[rt] = seen(j0, kb, rt);
+#pragma unroll 1
+            for (int kk = 0; kk < 32; ++kk) {
+                const int j = j0 + kb * 32 + kk;
+                if (j >= s.ctx + s.n) break;
+                const char* vp;
+                if (j < s.ctx) {
+                    const int pg = (int)quot(a.page, j);
+                    const int id = a.table[(int64_t)b * a.width + pg];
+                    if ((uint32_t)id >= (uint32_t)a.n_pages) continue;
+                    vp = a.vp.p + id * a.vp.page + (j - pg * (int)a.page.d) * a.vp.row + h * a.vp.head;
+                } else {
+                    vp = a.v.p + (s.row0 + (j - s.ctx)) * a.v.row + h * a.v.head;
+                }
+#pragma unroll
+                for (int dt = 0; dt < DT; ++dt) {
+                    const int e = dt * 16 + 4 * g;
+                    const char* at = vp + (e < a.d ? e : 0) * ES;      // columns past d are not written
+                    f32x4 v;
+                    if constexpr (C::IO == GDN_F32)
+                        v = *(const f32x4*)at;
+                    else
+                        v = __builtin_convertvector(*(const bf16x4*)at, f32x4);
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[rt][dt][i] += ((bits[rt] >> kk) & 1u) && nonfinite(v[i]) ? v[i] : 0.f;
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+
+    // Tiles [t0, t1) of the block.
+    __device__ __forceinline__ void run(int t0, int t1) {
+        if (threadIdx.x < C::STAGES * C::WK) s_flag[threadIdx.x] = 0;
+        __syncthreads();                     // also: the last run's LDS is done with
+        fetch_pages(t0);
+        load(t0);
+        if (t0 + 1 < t1) fetch_pages(t0 + 1);
+        store(t0, 0);
+        int stage = 0;
+        for (int t = t0; t < t1; ++t) {
+            const bool more = t + 1 < t1;
+            if (more) {
+                load(t + 1);
+                if (t + 2 < t1) fetch_pages(t + 2);
+            }
+            if constexpr (C::WR > 1) __syncthreads();
+            compute(t, stage);
+            if constexpr (C::WR > 1) stage ^= 1;
+            if (more) store(t + 1, stage);
+        }
+    }
+
+    // Joins the waves that split the keys.  Afterwards wave wk holds the columns of its share in
+    // acc[rt][0 .. DQ), and every wave has the rows' m and l.
+    __device__ __forceinline__ void join_waves() {
+        const int c16 = lane & 15;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            l[rt] += __shfl_xor(l[rt], 16);
+            l[rt] += __shfl_xor(l[rt], 32);
+        }
+        bad = __syncthreads_or(bad) != 0;
+        if constexpr (C::WK > 1) {
+            float* ml = (float*)lds;                    // [WK][WR RT 16][2]
+            constexpr int ROWS = C::WR * RT * 16;
+            const int r0 = wr * RT * 16 + c16;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                if (lane < 16) {
+                    ml[(wk * ROWS + r0 + rt * 16) * 2] = m[rt];
+                    ml[(wk * ROWS + r0 + rt * 16) * 2 + 1] = l[rt];
+                }
+            __syncthreads();
+            float w[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float mm[C::WK], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < C::WK; ++k) {
+                    mm[k] = ml[(k * ROWS + r0 + rt * 16) * 2];
+                    top = fmaxf(top, mm[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < C::WK; ++k)
+                    sum += ml[(k * ROWS + r0 + rt * 16) * 2 + 1] * weight(mm[k], top);
+                w[rt] = weight(m[rt], top);
+                m[rt] = top;
+                l[rt] = sum;
+            }
+            f32x4* part = (f32x4*)(lds + C::WK * ROWS * 8);   // [WK][WR][RT][DQ][64]
+            f32x4 mine[RT][C::DQ];
+#pragma unroll
+            for (int k = 0; k < C::WK; ++k) {
+                if (k > 0) __syncthreads();
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int dq = 0; dq < C::DQ; ++dq)
+                        part[(((wk * C::WR + wr) * RT + rt) * C::DQ + dq) * 64 + lane] = acc[rt][k * C::DQ + dq] * w[rt];
+                __syncthreads();
+                if (wk == k) {
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                        for (int dq = 0; dq < C::DQ; ++dq) {
+                            f32x4 x = zero4();
+#pragma unroll
+                            for (int j = 0; j < C::WK; ++j)
+                                x += part[(((j * C::WR + wr) * RT + rt) * C::DQ + dq) * 64 + lane];
+                            mine[rt][dq] = x;
+                        }
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = mine[rt][dq];
+        }
+        if (bad) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) l[rt] = __uint_as_float(0x7fc00000u);
+        }
+    }
+
+    // 2^(m - top) of partial results; those of no visible key (m = -inf) weigh nothing.
+    static __device__ __forceinline__ float weight(float m, float top) {
+        return m == -INFINITY ? 0.f : exp2_fast(m - top);
+    }
+
+    // Rows of the block to o: acc[rt][0 .. DQ) / l.
+    __device__ __forceinline__ void write(int block, bool poison) {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int r = row_of(block, rt);
+            if (r >= s.n * a.group) continue;
+            const int i = (int)quot(a.group_div, r);
+            char* p = a.o.p + (s.row0 + i) * a.o.row + (h * a.group + (r - i * a.group)) * a.o.head;
+            const float inv = 1.f / l[rt];
+#pragma unroll
+            for (int dq = 0; dq < C::DQ; ++dq) {
+                const int e = (wk * C::DQ + dq) * 16 + 4 * g;
+                if (e >= a.d) continue;
+                f32x4 x = acc[rt][dq] * inv;
+                if (poison) x = f32x4{1.f, 1.f, 1.f, 1.f} * __uint_as_float(0x7fc00000u);
+                if constexpr (C::IO == GDN_F32)
+                    *(f32x4*)(p + e * ES) = x;
+                else
+                    *(bf16x4*)(p + e * ES) = __builtin_convertvector(x, bf16x4);
+            }
+        }
+    }
+
+    // Partial results in the lanes' own order: [WR RT][DT][64] columns, then m and l by row.
+    __device__ __forceinline__ f32x4* slot_acc(char* slot, int rt, int dq) const {
+        return (f32x4*)slot + ((wr * RT + rt) * DT + wk * C::DQ + dq) * 64 + lane;
+    }
+    __device__ __forceinline__ float* slot_ml(char* slot, int rt) const {
+        return (float*)(slot + C::BM * C::D * 4) + ((wr * RT + rt) * 16 + (lane & 15)) * 2;
+    }
+    __device__ __forceinline__ void save(char* slot) const {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int dq = 0; dq < C::DQ; ++dq) *slot_acc(slot, rt, dq) = acc[rt][dq];
+            if (wk == 0 && lane < 16) {
+                float* ml = slot_ml(slot, rt);
+                ml[0] = m[rt];
+                ml[1] = l[rt];
+            }
+        }
+    }
+    // Parts 0 .. n - 1 of a block, in the order of their keys; slot_of(i) is part i's place.
+    template <class F>
+    __device__ __forceinline__ void join_parts(int n, F slot_of) {
+        float top[RT], sum[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            top[rt] = -INFINITY;
+            sum[rt] = 0.f;
+#pragma unroll
+            for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = zero4();
+        }
+        for (int i = 0; i < n; ++i)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) top[rt] = fmaxf(top[rt], slot_ml(slot_of(i), rt)[0]);
+        for (int i = 0; i < n; ++i) {
+            char* slot = slot_of(i);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const float* ml = slot_ml(slot, rt);
+                const float w = weight(ml[0], top[rt]);
+                sum[rt] += ml[1] * w;
+#pragma unroll
+                for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] += *slot_acc(slot, rt, dq) * w;
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) l[rt] = sum[rt];
+    }
+};
+
+template <class C>
+__global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan plan) {
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    __shared__ int64_t s_pre[kThreads];
+    __shared__ int64_t s_part[kThreads / 64];
+    __shared__ int s_max[kThreads / 64];
+    __shared__ int s_flag[2 * 4];
+    __shared__ int s_pick, s_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // Neighbouring shares on one XCD, whose L2 then holds the keys that they have in common.
+    const int per = plan.grid / kXcds;
+    const int logical = (int)(blockIdx.x % kXcds) * per + (int)(blockIdx.x / kXcds);
+    const int cluster = logical / plan.side, member = logical % plan.side;
+    if (cluster >= plan.clusters) return;
+
+    // The line of tiles: sequence b owns Hk groups tiles of it.  Its length, and the longest block.
+    int64_t total = 0;
+    int longest = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        int64_t x = 0;
+        int t = 0;
+        if (b0 + tid < a.B) {
+            const Seq s = load_seq<C>(a, plan.side, b0 + tid);
+            t = s.tiles;
+            x = (int64_t)a.Hk * s.groups * s.tiles;
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t y = __shfl_up(x, o);
+            if (lane >= o) x += y;
+            t = max(t, __shfl_xor(t, o));
+        }
+        if (lane == 63) s_part[wave] = x;
+        if (lane == 0) s_max[wave] = t;
+        __syncthreads();
+        int64_t base = total;
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w < wave) base += s_part[w];
+            total += s_part[w];
+            longest = max(longest, s_max[w]);
+        }
+        s_pre[tid] = base + x;               // kept where one round covers the batch
+        __syncthreads();
+    }
+    const int64_t share = max((total + plan.clusters - 1) / plan.clusters,
+                              (int64_t)((longest + kMaxParts - 2) / (kMaxParts - 1)));
+    int64_t at = cluster * share;
+    const int64_t end = min(total, at + share);
+    if (at >= end) return;
+
+    // The sequence in which the share begins, and where that sequence begins on the line.
+    int b = 0;
+    int64_t start = 0;
+    if (a.B <= kThreads) {
+        const int n = __popcll(__ballot(tid < a.B && s_pre[tid] <= at));
+        if (lane == 0) s_max[wave] = n;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreads / 64; ++w) b += s_max[w];
+        start = b > 0 ? s_pre[b - 1] : 0;
+    } else {
+        // many sequences: walk the line again, a round at a time
+        if (tid == 0) s_pick = -1;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            int64_t x = 0, own = 0;
+            if (b0 + tid < a.B) {
+                const Seq s = load_seq<C>(a, plan.side, b0 + tid);
+                x = own = (int64_t)a.Hk * s.groups * s.tiles;
+            }
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int64_t y = __shfl_up(x, o);
+                if (lane >= o) x += y;
+            }
+            __syncthreads();
+            if (lane == 63) s_part[wave] = x;
+            __syncthreads();
+            int64_t base = start, sum = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 64; ++w) {
+                if (w < wave) base += s_part[w];
+                sum += s_part[w];
+            }
+            const int64_t hi = base + x, lo = hi - own;
+            if (own > 0 && lo <= at && at < hi) {
+                s_pick = b0 + tid;
+                s_pre[0] = lo;
+            }
+            __syncthreads();
+            if (s_pick >= 0) break;
+            start += sum;
+        }
+        b = s_pick;
+        start = s_pre[0];
+    }
+
+    Worker<C> w(a, lds, s_flag);
+    while (at < end) {
+        b = __builtin_amdgcn_readfirstlane(b);
+        w.b = b;
+        w.s = load_seq<C>(a, plan.side, b);
+        const int64_t units = (int64_t)a.Hk * w.s.groups;
+        while (at < end && at - start < units * w.s.tiles) {
+            const int64_t unit = (at - start) / w.s.tiles;
+            const int64_t us = start + unit * w.s.tiles, ue = us + w.s.tiles;
+            w.h = (int)(unit / w.s.groups);
+            const int block = (int)(unit - (int64_t)w.h * w.s.groups) * plan.side + member;
+            const int64_t stop = min(end, ue);
+            if (block < w.s.blocks) {
+                w.begin(block);
+                if (!w.s.poison) w.run((int)(at - us), (int)(stop - us));
+                w.join_waves();
+                const int64_t c0 = us / share, c1 = (ue - 1) / share;
+                bool out = c0 == c1;
+                if (!out) {
+                    auto slot = [&](int64_t c) {
+                        return plan.slots + ((c * plan.side + member) * 2 + (c == c0 ? 1 : 0)) * (int64_t)C::SLOT;
+                    };
+                    w.save(slot(cluster));
+                    __threadfence();
+                    __syncthreads();
+                    int32_t* arrived = plan.arrived + ((int64_t)b * a.Hk + w.h) * plan.max_blocks + block;
+                    const int parts = (int)(c1 - c0) + 1;
+                    if (tid == 0) s_last = atomicAdd(arrived, 1) == parts - 1;
+                    __syncthreads();
+                    out = s_last != 0;
+                    if (out) {
+                        __threadfence();
+                        w.join_parts(parts, [&](int i) { return slot(c0 + i); });
+                        if (tid == 0) *arrived = 0;
+                    }
+                }
+                if (out) w.write(block, w.s.poison);
+            }
+            at = stop;
+        }
+        start += units * w.s.tiles;
+        ++b;
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+template <class C>
+inline Plan make_plan(int B, int N, int group, int Hk, bool dense, char* ws) {
+    Plan p;
+    p.grid = kCUs * C::OCC;
+    const int blocks = (N * group + C::BM - 1) / C::BM;
+    // Blocks of rows of one (sequence, key head) side by side over the same keys, up to eight,
+    // so that they find the keys in L2.  Trees of different sizes would leave members idle:
+    // there the blocks follow each other.
+    const int rounds = (blocks + 7) / 8;
+    p.side = dense ? (blocks + rounds - 1) / rounds : 1;
+    p.clusters = p.grid / p.side;
+    p.max_blocks = blocks;
+    const size_t counters = ((size_t)B * Hk * blocks * 4 + 255) / 256 * 256;
+    p.arrived = (int32_t*)ws;
+    p.slots = ws + counters;
+    return p;
+}
+
+template <class C>
+inline size_t plan_bytes(int B, int N, int group, int Hk) {
+    const Plan p = make_plan<C>(B, N, group, Hk, true, nullptr);
+    return (size_t)(p.slots - (char*)p.arrived) + (size_t)p.grid * 2 * C::SLOT;
+}
+
+template <class C>
+inline hipError_t launch_cfg(const AttnArgs& a, hipStream_t stream) {
+    const Plan p = make_plan<C>(a.B, a.N, a.group, a.Hk, a.offsets == nullptr, a.ws);
+    return launch(attn_kernel<C>, dim3((unsigned)p.grid), dim3(kThreads), C::LDS, stream, a, p);
+}
+
+// The shape of the tiles by the rows that share keys, N group; f(Cfg) is called with the one
+// that applies.  Few rows: the waves split the keys and every key is read once, from memory
+// to registers to LDS, without a barrier.  Many rows: the waves split the rows and share
+// each tile; 64 rows per wave halve the LDS reads of 32.
+template <int IO, int D, class F>
+inline auto choose(int rows, F f) {
+    if constexpr (IO == GDN_F32) {
+        // 256 columns of fp32 for four waves' own keys would not fit the LDS
+        if (rows <= 16 && D <= 128) return f(Cfg<IO, D, 1, (D > 128 ? 4 : 1), 32, (D <= 64 ? 2 : 1)>{});
+        return f(Cfg<IO, D, 1, 4, 32, (D <= 128 ? 2 : 1)>{});
+    } else {
+        constexpr int occ = D <= 128 ? 2 : 1;
+        if (rows <= 16) return f(Cfg<IO, D, 1, 1, 32, occ>{});
+        if (rows <= 32) return f(Cfg<IO, D, 2, 1, 32, occ>{});
+        if (rows <= 64) return f(Cfg<IO, D, 2, 2, 32, occ>{});
+        if (rows <= 128 || D > 128) return f(Cfg<IO, D, 2, 4, (D > 128 ? 32 : 64), occ>{});
+        return f(Cfg<IO, D, (D > 128 ? 2 : 4), 4, (D > 128 ? 32 : 64), 1>{});
+    }
+}
+
+template <int IO, int D>
+inline hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
+    return choose<IO, D>(a.N * a.group, [&](auto c) { return launch_cfg<decltype(c)>(a, stream); });
+}
+template <int IO, int D>
+inline size_t bytes_d(int B, int N, int group, int Hk) {
+    return choose<IO, D>(N * group, [&](auto c) { return plan_bytes<decltype(c)>(B, N, group, Hk); });
+}
+
+}  // namespace attn
+
+// One translation unit each (compiled in parallel).
+hipError_t attn_launch_bf16_64(const AttnArgs& a, hipStream_t stream);
+hipError_t attn_launch_bf16_128(const AttnArgs& a, hipStream_t stream);
+hipError_t attn_launch_bf16_256(const AttnArgs& a, hipStream_t stream);
+hipError_t attn_launch_f32_64(const AttnArgs& a, hipStream_t stream);
+hipError_t attn_launch_f32_128(const AttnArgs& a, hipStream_t stream);
+hipError_t attn_launch_f32_256(const AttnArgs& a, hipStream_t stream);
+size_t attn_bytes_bf16_64(int B, int N, int group, int Hk);
+size_t attn_bytes_bf16_128(int B, int N, int group, int Hk);
+size_t attn_bytes_bf16_256(int B, int N, int group, int Hk);
+size_t attn_bytes_f32_64(int B, int N, int group, int Hk);
+size_t attn_bytes_f32_128(int B, int N, int group, int Hk);
+size_t attn_bytes_f32_256(int B, int N, int group, int Hk);
+
+}  // namespace gdn
