@@ -179,7 +179,9 @@ int gdn_attn_verify(const gdn_attn_dims* dims, const int32_t* offsets, const gdn
     if (rc) return rc;
     const int group = dims->h_q / dims->h_kv, es = elem(dims->io_dtype);
     auto rows_bytes = [es](const gdn_attn_rows* r) { return Rows{(char*)r->data, r->row * es, r->head * es}; };
-    auto pool_bytes = [es](Pool p) { return Pool{p.p, p.page * es, p.row * es, p.head * es}; };
+    auto pool_bytes = [es](Pool p) { return Pool{p.p, p.page * es / 16, p.row * es / 16, p.head * es}; };
+    for (int64_t x : {cache->k_page, cache->v_page, cache->k_row, cache->v_row})
+        if (x * es / 16 > 0xffffffffLL) return GDN_ERR_DIMS;
     AttnArgs a{dims->batch, dims->n_nodes, dims->h_q, dims->h_kv, group, dims->d, cache->n_pages, width,
                (dims->n_nodes + 31) / 32, dims->scale, fast_div(cache->page_rows), fast_div(group), offsets,
                pool_bytes(key_pool(cache, layer)), pool_bytes(value_pool(cache, layer)), rows_bytes(q), rows_bytes(k),

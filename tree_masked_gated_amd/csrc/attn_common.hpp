@@ -110,8 +110,8 @@ struct AttnArgs {
     float scale;
     FastDiv page, group_div;
     const int32_t* offsets;
-    Pool kp, vp;                             // strides in bytes, here and in the rows
-    Rows q, k, v, o;
+    Pool kp, vp;                             // page and row in pieces of 16 bytes, head in bytes
+    Rows q, k, v, o;                         // strides in bytes
     const int32_t* table;
     const int32_t* ctx;
     const uint32_t* anc;

@@ -35,7 +35,6 @@ namespace gdn {
 namespace attn {
 
 constexpr int kCUs = 256, kXcds = 8;
-constexpr int kThreads = 256;
 constexpr int kMaxCtx = 0x7fff0000;          // key indexes, whole tiles of them, are 32 bits
 constexpr float kLag = 8.0f;
 constexpr int kMaxParts = 64;                // pieces of one block of rows
@@ -47,12 +46,13 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// IO, D: element type and head size (padded with zeros); RT: tiles of 16 rows per wave;
-// WR: waves side by side over rows, WK = 4 / WR over keys; KT: keys per wave and step.
-template <int IO_, int D_, int RT_, int WR_, int KT_, int OCC_>
+// IO, D: element type and head size (padded with zeros); RT: tiles of 16 rows per wave; WR waves
+// side by side over rows, WK over keys; KT: keys per wave and step; OCC: workgroups per CU.
+template <int IO_, int D_, int RT_, int WR_, int WK_, int KT_, int OCC_>
 struct Cfg {
-    static constexpr int IO = IO_, D = D_, RT = RT_, WR = WR_, KT = KT_, OCC = OCC_;
-    static constexpr int WK = 4 / WR;
+    static constexpr int IO = IO_, D = D_, RT = RT_, WR = WR_, WK = WK_, KT = KT_, OCC = OCC_;
+    static constexpr int NT = 64 * WR * WK;             // threads
+    static constexpr int WAVES = NT / 256 * OCC;        // per SIMD
     static constexpr int ES = IO == GDN_F32 ? 4 : 2;
     static constexpr int E = 16 / ES;                   // elements of a 16-byte piece
     static constexpr int CPR = D / E;                   // pieces of a row
@@ -71,7 +71,7 @@ struct Cfg {
     static constexpr int SLOT = BM * (D + 2) * 4;       // bytes of a partial result
     static_assert(LDS + 4096 <= kMaxLds, "LDS of a workgroup");
     static_assert(TG % CPR == 0 && NCH >= 1, "a thread keeps its piece of the row");
-    static_assert(KT % 32 == 0 && KT <= 64, "mask words");
+    static_assert(KT % 32 == 0 && DT % WK == 0, "mask words, columns of the joining waves");
 };
 
 // Launch parameters that depend on the configuration.
@@ -160,7 +160,7 @@ struct Worker {
 
     const AttnArgs& a;
     char* lds;
-    int* s_flag;                             // [2]: a tile's V holds infinities or NaN
+    int* s_flag;                             // [WK]: a tile's V holds infinities or NaN
     int lane, wr, wk, tg;                    // tg: thread within its key group
     int b, h;
     Seq s;
@@ -171,6 +171,10 @@ struct Worker {
     int node[RT];
     uint4 kreg[NCH], vreg[NCH];
     int pid[NCH];
+    const char* kbase;                       // this thread's piece of row 0 of page 0
+    const char* vbase;
+    const int32_t* page_table;
+    uint32_t top_page;                       // the largest page id met, as unsigned
     bool bad;
 
     __device__ __forceinline__ Worker(const AttnArgs& a_, char* lds_, int* flag) : a(a_), lds(lds_), s_flag(flag) {
@@ -216,74 +220,66 @@ struct Worker {
     // First key of this wave's part of tile t.
     __device__ __forceinline__ int key0(int t) const { return t * C::KW + wk * C::KT; }
 
+    // Page ids of a tile of the prefix.
     __device__ __forceinline__ void fetch_pages(int t) {
         const int j0 = key0(t) + tg / C::CPR;
 #pragma unroll
+        for (int i = 0; i < NCH; ++i) pid[i] = page_table[quot(a.page, j0 + i * C::KSTEP)];
+    }
+
+    // Byte offset of row r of page id in a pool, in pieces of 16.
+    static __device__ __forceinline__ uint64_t offset16(const Pool& pool, uint32_t id, uint32_t r) {
+        return (uint64_t)id * (uint32_t)pool.page + (uint64_t)r * (uint32_t)pool.row;
+    }
+
+    // Loads a tile of the prefix into registers, through the page ids fetched before.
+    __device__ __forceinline__ void load(int t) {
+        const int j0 = key0(t) + tg / C::CPR;
+#pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            const int j = j0 + i * C::KSTEP;
-            pid[i] = 0;
-            if (j < s.ctx) pid[i] = a.table[(int64_t)b * a.width + quot(a.page, j)];
+            const uint32_t j = j0 + i * C::KSTEP;
+            const uint32_t r = j - quot(a.page, j) * a.page.d;
+            top_page = max(top_page, (uint32_t)pid[i]);
+            const uint32_t id = min((uint32_t)pid[i], (uint32_t)a.n_pages - 1u);
+            kreg[i] = *(const uint4*)(kbase + (offset16(a.kp, id, r) << 4));
+            vreg[i] = *(const uint4*)(vbase + (offset16(a.vp, id, r) << 4));
         }
     }
 
-    // Loads tile t into registers, through the page ids fetched before.  Every load is made; one
-    // that has no row reads the pool's first row, and store() drops what it brought.
-    __device__ __forceinline__ void load(int t) {
+    // The same for a tile that reaches the tree's own rows, or past them.
+    __device__ __forceinline__ void load_mixed(int t) {
         const int c = tg % C::CPR;
         const int j0 = key0(t) + tg / C::CPR;
         const int64_t in_row = c * E < a.d ? c * 16 : 0;
-        const char* kb = a.kp.p + h * a.kp.head + in_row;
-        const char* vb = a.vp.p + h * a.vp.head + in_row;
-        if (!mixed(t)) {
+        bool any = false;
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int j = j0 + i * C::KSTEP;
-                const int r = j - (int)quot(a.page, j) * (int)a.page.d;
-                const bool ok = (uint32_t)pid[i] < (uint32_t)a.n_pages;
-                bad |= !ok;
-                const int64_t id = ok ? pid[i] : 0;
-                kreg[i] = *(const uint4*)(kb + id * a.kp.page + r * a.kp.row);
-                vreg[i] = *(const uint4*)(vb + id * a.vp.page + r * a.vp.row);
+        for (int i = 0; i < NCH; ++i) {
+            const int j = j0 + i * C::KSTEP;
+            kreg[i] = vreg[i] = uint4{0, 0, 0, 0};
+            if (j < s.ctx) {
+                const uint32_t pg = quot(a.page, j);
+                const uint32_t at = page_table[pg];
+                top_page = max(top_page, at);
+                const uint32_t id = min(at, (uint32_t)a.n_pages - 1u), r = j - pg * a.page.d;
+                kreg[i] = *(const uint4*)(kbase + (offset16(a.kp, id, r) << 4));
+                vreg[i] = *(const uint4*)(vbase + (offset16(a.vp, id, r) << 4));
+            } else if (j < s.ctx + s.n) {
+                const int64_t r = s.row0 + (j - s.ctx);
+                kreg[i] = *(const uint4*)(a.k.p + h * a.k.head + in_row + r * a.k.row);
+                vreg[i] = *(const uint4*)(a.v.p + h * a.v.head + in_row + r * a.v.row);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                const int j = j0 + i * C::KSTEP;
-                const bool prefix = j < s.ctx, tree = !prefix && j < s.ctx + s.n;
-                const int r = prefix ? j - (int)quot(a.page, j) * (int)a.page.d : 0;
-                const bool ok = !prefix || (uint32_t)pid[i] < (uint32_t)a.n_pages;
-                bad |= !ok;
-                const int64_t id = prefix && ok ? pid[i] : 0;
-                const int64_t tr = s.row0 + (j - s.ctx);
-                const char* kq = kb + id * a.kp.page + r * a.kp.row;
-                const char* vq = vb + id * a.vp.page + r * a.vp.row;
-                const char* kt = a.k.p + h * a.k.head + in_row + tr * a.k.row;
-                const char* vt = a.v.p + h * a.v.head + in_row + tr * a.v.row;
-                kreg[i] = *(const uint4*)(tree ? kt : kq);
-                vreg[i] = *(const uint4*)(tree ? vt : vq);
-            }
+            // A zero weight times an infinity is no zero: what is not finite is kept out of the
+            // product and added to the rows that see it (spread()).
+            any |= clean<C::IO>(vreg[i]);
         }
+        if (any) s_flag[wk] = 1;
     }
 
-    // Whether this wave's part of tile t reaches the tree's own keys.
-    __device__ __forceinline__ bool mixed(int t) const { return key0(t) + C::KT > s.ctx; }
-
     // Registers to LDS.
-    __device__ __forceinline__ void store(int t, int stage) {
+    __device__ __forceinline__ void store(int stage) {
         char* kt = ktile(stage);
         char* vt = vtile(stage);
         const int c = tg % C::CPR, k0 = tg / C::CPR;
-        if (mixed(t)) {
-            // A zero weight times an infinity is no zero: what is not finite is kept out of the
-            // product and added to the rows that see it (spread()).
-            bool any = false;
-#pragma unroll
-            for (int i = 0; i < NCH; ++i) {
-                if (key0(t) + k0 + i * C::KSTEP >= s.ctx + s.n) vreg[i] = uint4{0, 0, 0, 0};
-                any |= clean<C::IO>(vreg[i]);
-            }
-            if (any) s_flag[stage * C::WK + wk] = 1;
-        }
         const bool pad = c * E >= a.d;       // columns past d: the query's are zero, the key's must be finite
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
@@ -311,6 +307,7 @@ struct Worker {
         return left < 32 ? x & ((1u << left) - 1u) : x;
     }
 
+    template <bool MIXED>
     __device__ __forceinline__ void compute(int t, int stage) {
         const int g = lane >> 4, c16 = lane & 15;
         const char* kt = ktile(stage);
@@ -341,8 +338,7 @@ struct Worker {
             }
         }
         const int j0 = key0(t);
-        const bool masked = mixed(t);
-        if (masked) {
+        if constexpr (MIXED) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
@@ -456,7 +452,9 @@ struct Worker {
                 }
             }
         }
-        if (masked && s_flag[stage * C::WK + wk] != 0) spread(j0);
+        if constexpr (MIXED) {
+            if (s_flag[wk] != 0) spread(j0);
+        }
     }
 
     // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
@@ -477,7 +475,7 @@ struct Worker {
                     const int pg = (int)quot(a.page, j);
                     const int id = a.table[(int64_t)b * a.width + pg];
                     if ((uint32_t)id >= (uint32_t)a.n_pages) continue;
-                    vp = a.vp.p + id * a.vp.page + (j - pg * (int)a.page.d) * a.vp.row + h * a.vp.head;
+                    vp = a.vp.p + (int64_t)h * a.vp.head + (offset16(a.vp, id, j - pg * (int)a.page.d) << 4);
                 } else {
                     vp = a.v.p + (s.row0 + (j - s.ctx)) * a.v.row + h * a.v.head;
                 }
@@ -501,26 +499,46 @@ struct Worker {
         }
     }
 
-    // Tiles [t0, t1) of the block.
+    // Tiles [t0, t1) of the block: those of the prefix alone, the next one's loads under way while
+    // one is computed, then the few that reach the tree's own rows, one after the other.
     __device__ __forceinline__ void run(int t0, int t1) {
-        if (threadIdx.x < C::STAGES * C::WK) s_flag[threadIdx.x] = 0;
-        __syncthreads();                     // also: the last run's LDS is done with
-        fetch_pages(t0);
-        load(t0);
-        if (t0 + 1 < t1) fetch_pages(t0 + 1);
-        store(t0, 0);
-        int stage = 0;
-        for (int t = t0; t < t1; ++t) {
-            const bool more = t + 1 < t1;
-            if (more) {
+        const int c = tg % C::CPR;
+        const int in_row = c * E < a.d ? c * 16 : 0;
+        kbase = a.kp.p + (int64_t)h * a.kp.head + in_row;
+        vbase = a.vp.p + (int64_t)h * a.vp.head + in_row;
+        page_table = a.table + (int64_t)b * a.width;
+        top_page = 0;
+        __syncthreads();                     // the last run's LDS is done with
+        const int full = min(t1, s.ctx / C::KW);
+        int t = t0;
+        if (t < full) {
+            int stage = 0;
+            fetch_pages(t);
+            load(t);
+            if (t + 1 < full) fetch_pages(t + 1);
+            store(0);
+            for (; t + 1 < full; ++t) {
                 load(t + 1);
-                if (t + 2 < t1) fetch_pages(t + 2);
+                fetch_pages(min(t + 2, full - 1));
+                if constexpr (C::WR > 1) __syncthreads();
+                compute<false>(t, stage);
+                if constexpr (C::STAGES > 1) stage ^= 1;
+                store(stage);
             }
             if constexpr (C::WR > 1) __syncthreads();
-            compute(t, stage);
-            if constexpr (C::WR > 1) stage ^= 1;
-            if (more) store(t + 1, stage);
+            compute<false>(t, stage);
+            ++t;
         }
+        for (; t < t1; ++t) {
+            __syncthreads();
+            if (threadIdx.x < C::WK) s_flag[threadIdx.x] = 0;
+            __syncthreads();
+            load_mixed(t);
+            store(0);
+            __syncthreads();
+            compute<true>(t, 0);
+        }
+        bad = top_page >= (uint32_t)a.n_pages;
     }
 
     // Joins the waves that split the keys.  Afterwards wave wk holds the columns of its share in
@@ -674,11 +692,11 @@ struct Worker {
 };
 
 template <class C>
-__global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan plan) {
+__global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan plan) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    __shared__ int64_t s_pre[kThreads];
-    __shared__ int64_t s_part[kThreads / 64];
-    __shared__ int s_max[kThreads / 64];
+    __shared__ int64_t s_pre[C::NT];
+    __shared__ int64_t s_part[C::NT / 64];
+    __shared__ int s_max[C::NT / 64];
     __shared__ int s_flag[2 * 4];
     __shared__ int s_pick, s_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -691,7 +709,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan
     // The line of tiles: sequence b owns Hk groups tiles of it.  Its length, and the longest block.
     int64_t total = 0;
     int longest = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += C::NT) {
         int64_t x = 0;
         int t = 0;
         if (b0 + tid < a.B) {
@@ -710,7 +728,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan
         __syncthreads();
         int64_t base = total;
 #pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) {
+        for (int w = 0; w < C::NT / 64; ++w) {
             if (w < wave) base += s_part[w];
             total += s_part[w];
             longest = max(longest, s_max[w]);
@@ -727,17 +745,17 @@ __global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan
     // The sequence in which the share begins, and where that sequence begins on the line.
     int b = 0;
     int64_t start = 0;
-    if (a.B <= kThreads) {
+    if (a.B <= C::NT) {
         const int n = __popcll(__ballot(tid < a.B && s_pre[tid] <= at));
         if (lane == 0) s_max[wave] = n;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kThreads / 64; ++w) b += s_max[w];
+        for (int w = 0; w < C::NT / 64; ++w) b += s_max[w];
         start = b > 0 ? s_pre[b - 1] : 0;
     } else {
         // many sequences: walk the line again, a round at a time
         if (tid == 0) s_pick = -1;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        for (int b0 = 0; b0 < a.B; b0 += C::NT) {
             int64_t x = 0, own = 0;
             if (b0 + tid < a.B) {
                 const Seq s = load_seq<C>(a, plan.side, b0 + tid);
@@ -753,7 +771,7 @@ __global__ __launch_bounds__(kThreads, C::OCC) void attn_kernel(AttnArgs a, Plan
             __syncthreads();
             int64_t base = start, sum = 0;
 #pragma unroll
-            for (int w = 0; w < kThreads / 64; ++w) {
+            for (int w = 0; w < C::NT / 64; ++w) {
                 if (w < wave) base += s_part[w];
                 sum += s_part[w];
             }
@@ -844,26 +862,32 @@ inline size_t plan_bytes(int B, int N, int group, int Hk) {
 template <class C>
 inline hipError_t launch_cfg(const AttnArgs& a, hipStream_t stream) {
     const Plan p = make_plan<C>(a.B, a.N, a.group, a.Hk, a.offsets == nullptr, a.ws);
-    return launch(attn_kernel<C>, dim3((unsigned)p.grid), dim3(kThreads), C::LDS, stream, a, p);
+    return launch(attn_kernel<C>, dim3((unsigned)p.grid), dim3(C::NT), C::LDS, stream, a, p);
 }
 
 // The shape of the tiles by the rows that share keys, N group; f(Cfg) is called with the one
 // that applies.  Few rows: the waves split the keys and every key is read once, from memory
 // to registers to LDS, without a barrier.  Many rows: the waves split the rows and share
-// each tile; 64 rows per wave halve the LDS reads of 32.
+// each tile.
 template <int IO, int D, class F>
 inline auto choose(int rows, F f) {
     if constexpr (IO == GDN_F32) {
         // 256 columns of fp32 for four waves' own keys would not fit the LDS
-        if (rows <= 16 && D <= 128) return f(Cfg<IO, D, 1, (D > 128 ? 4 : 1), 32, (D <= 64 ? 2 : 1)>{});
-        return f(Cfg<IO, D, 1, 4, 32, (D <= 128 ? 2 : 1)>{});
+        if constexpr (D <= 128) {
+            if (rows <= 16) return f(Cfg<IO, D, 1, 1, 4, 32, (D <= 64 ? 2 : 1)>{});
+        }
+        return f(Cfg<IO, D, 1, 4, 1, 32, (D <= 128 ? 2 : 1)>{});
     } else {
         constexpr int occ = D <= 128 ? 2 : 1;
-        if (rows <= 16) return f(Cfg<IO, D, 1, 1, 32, occ>{});
-        if (rows <= 32) return f(Cfg<IO, D, 2, 1, 32, occ>{});
-        if (rows <= 64) return f(Cfg<IO, D, 2, 2, 32, occ>{});
-        if (rows <= 128 || D > 128) return f(Cfg<IO, D, 2, 4, (D > 128 ? 32 : 64), occ>{});
-        return f(Cfg<IO, D, (D > 128 ? 2 : 4), 4, (D > 128 ? 32 : 64), 1>{});
+        if (rows <= 16) return f(Cfg<IO, D, 1, 1, 4, 32, occ>{});
+        if (rows <= 32) return f(Cfg<IO, D, 2, 1, 4, 32, occ>{});
+        if (rows <= 64) return f(Cfg<IO, D, 2, 2, 2, 32, occ>{});
+        if constexpr (D > 128) {
+            return f(Cfg<IO, D, 2, 4, 1, 32, 1>{});
+        } else {
+            if (rows <= 128) return f(Cfg<IO, D, 2, 4, 1, 64, 2>{});
+            return f(Cfg<IO, D, 2, 8, 1, 64, 1>{});
+        }
     }
 }
 
