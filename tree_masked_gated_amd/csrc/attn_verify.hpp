@@ -40,6 +40,7 @@ constexpr float kLag = 8.0f;
 constexpr int kMaxParts = 64;                // pieces of one block of rows
 constexpr float kLog2e = 1.4426950408889634f;
 
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -167,7 +168,8 @@ struct Worker {
 
     typename std::conditional<C::IO == GDN_F32, f32x4[C::D / 16], bf16x8[C::D / 32]>::type q[RT];
     f32x4 acc[RT][DT];
-    float m[RT], l[RT];
+    // vectors, not arrays: the compiler keeps them in registers
+    float __attribute__((ext_vector_type(RT))) m, l;
     int node[RT];
     uint4 kreg[NCH], vreg[NCH];
     int pid[NCH];
@@ -186,10 +188,16 @@ struct Worker {
         tg = tid - wk * C::TG;
     }
 
+    // Addresses of the steps that follow are formed anew from here on.  Without this the compiler
+    // forms those of every step once, ahead of all of them, and has no registers left for the
+    // loop over the prefix.
+    __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(lane), "+v"(tg)); }
+
     __device__ __forceinline__ char* ktile(int stage) const { return lds + (stage * C::WK + wk) * 2 * C::TILEB; }
     __device__ __forceinline__ char* vtile(int stage) const { return ktile(stage) + C::TILEB; }
 
     __device__ __forceinline__ void begin(int block) {
+        fresh();
         const int g = lane >> 4;
         bad = false;
 #pragma unroll
@@ -307,12 +315,9 @@ struct Worker {
         return left < 32 ? x & ((1u << left) - 1u) : x;
     }
 
-    template <bool MIXED>
-    __device__ __forceinline__ void compute(int t, int stage) {
+    // Scores of a tile's keys, raw products.
+    __device__ __forceinline__ void scores(const char* kt, f32x4 (&sc)[RT][KTILES]) const {
         const int g = lane >> 4, c16 = lane & 15;
-        const char* kt = ktile(stage);
-        const char* vt = vtile(stage);
-        f32x4 sc[RT][KTILES];
 #pragma unroll
         for (int x = 0; x < KTILES; ++x) {
             const char* row = kt + c16 * C::ROWB + x * 16 * C::ROWB;
@@ -337,22 +342,10 @@ struct Worker {
                 }
             }
         }
-        const int j0 = key0(t);
-        if constexpr (MIXED) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-                for (int kb = 0; kb < C::KT / 32; ++kb) {
-                    const uint32_t bits = seen(j0, kb, rt) >> (4 * g);
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (!((bits >> (16 * x + i)) & 1u)) sc[rt][2 * kb + x][i] = -INFINITY;
-                }
-            }
-        }
-        // running maximum, moved only where it lags too far
+    }
+
+    // Running maximum, moved only where it lags too far.
+    __device__ __forceinline__ void raise(const f32x4 (&sc)[RT][KTILES]) {
         const float scale = a.scale * kLog2e;
         float top[RT];
         bool move = false;
@@ -380,7 +373,13 @@ struct Worker {
                 for (int dt = 0; dt < DT; ++dt) acc[rt][dt] *= f;
             }
         }
-        typename std::conditional<C::IO == GDN_F32, f32x4, bf16x8>::type p[RT][C::IO == GDN_F32 ? KTILES : KTILES / 2];
+    }
+
+    // Weights of a tile's keys from their scores, and their sum.
+    typedef typename std::conditional<C::IO == GDN_F32, f32x4, bf16x8>::type Weights;
+    static constexpr int PX = C::IO == GDN_F32 ? KTILES : KTILES / 2;
+    __device__ __forceinline__ void weigh(f32x4 (&sc)[RT][KTILES], Weights (&p)[RT][PX]) {
+        const float scale = a.scale * kLog2e;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const float base = m[rt] == -INFINITY ? 0.f : m[rt];
@@ -414,6 +413,11 @@ struct Worker {
                 }
             }
         }
+    }
+
+    // acc += weights times a tile's values.
+    __device__ __forceinline__ void values(const char* vt, const Weights (&p)[RT][PX]) {
+        const int g = lane >> 4, c16 = lane & 15;
         if constexpr (C::IO == GDN_F32) {
 #pragma unroll
             for (int x = 0; x < KTILES; ++x)
@@ -452,9 +456,121 @@ struct Worker {
                 }
             }
         }
+    }
+
+    // A tile in LDS, all at once.
+    template <bool MIXED>
+    __device__ __forceinline__ void compute(int t, int stage) {
+        f32x4 sc[RT][KTILES];
+        scores(ktile(stage), sc);
+        const int j0 = key0(t);
+        if constexpr (MIXED) {
+            const int g = lane >> 4;
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+                for (int kb = 0; kb < C::KT / 32; ++kb) {
+                    const uint32_t bits = seen(j0, kb, rt) >> (4 * g);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((bits >> (16 * x + i)) & 1u)) sc[rt][2 * kb + x][i] = -INFINITY;
+                }
+            }
+        }
+        raise(sc);
+        Weights p[RT][PX];
+        weigh(sc, p);
+        values(vtile(stage), p);
         if constexpr (MIXED) {
             if (s_flag[wk] != 0) spread(j0);
         }
+    }
+
+    // Waves that share tiles: the pieces of a tile go from the pools to LDS without passing
+    // through registers.  A wave's 64 pieces land side by side, so that thread tg fills the place
+    // tg + i TG of the tile and fetches the piece that belongs there.  Keys are loaded two tiles
+    // ahead of the one whose values are being added, values one.
+    struct Ahead {
+        uint64_t k[NCH], v[NCH];             // offsets in pieces of 16 bytes from the pools' data
+    };
+    __device__ __forceinline__ int piece_at(int i) const {
+        return (tg % C::CPR) ^ swizzle<C>(tg / C::CPR + i * C::KSTEP);
+    }
+    __device__ __forceinline__ Ahead locate(int t) {
+        const int j0 = key0(t) + tg / C::CPR;
+        Ahead at;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const uint32_t j = j0 + i * C::KSTEP;
+            const uint32_t r = j - quot(a.page, j) * a.page.d;
+            top_page = max(top_page, (uint32_t)pid[i]);
+            const uint32_t id = min((uint32_t)pid[i], (uint32_t)a.n_pages - 1u);
+            at.k[i] = offset16(a.kp, id, r) + piece_at(i);
+            at.v[i] = offset16(a.vp, id, r) + piece_at(i);
+        }
+        return at;
+    }
+    __device__ __forceinline__ void to_lds(const char* base, const uint64_t (&at)[NCH], char* tile) const {
+        const uint32_t to = __builtin_amdgcn_readfirstlane(
+            (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)tile + wr * 1024);
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+            const char* from = base + (at[i] << 4);
+            if (piece_at(i) * E < a.d)       // LDS holds zeros where a row has ended
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                             :: "s"(to + i * C::TG * 16), "v"(from) : "memory");
+        }
+    }
+    // What this wave sent to LDS has arrived, and so has every other wave's.
+    static __device__ __forceinline__ void arrive() {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    }
+    __device__ __forceinline__ void run_prefix(int t0, int full) {
+        if (a.d < C::D) {
+            for (int i = threadIdx.x; i < C::LDS / 16; i += C::NT) ((uint4*)lds)[i] = uint4{0, 0, 0, 0};
+            __syncthreads();
+        }
+        const char* kb = a.kp.p + (int64_t)h * a.kp.head;
+        const char* vb = a.vp.p + (int64_t)h * a.vp.head;
+        fetch_pages(t0);
+        Ahead at = locate(t0);
+        to_lds(kb, at.k, ktile(0));
+        to_lds(vb, at.v, vtile(0));
+        fetch_pages(min(t0 + 1, full - 1));
+        at = locate(min(t0 + 1, full - 1));
+        fetch_pages(min(t0 + 2, full - 1));
+        f32x4 sc[RT][KTILES];
+        arrive();
+        to_lds(kb, at.k, ktile(1));
+        scores(ktile(0), sc);
+        int stage = 0;
+        for (int t = t0; t + 1 < full; ++t) {
+            arrive();
+            // K of t + 1 and V of t are there; K of t and V of t - 1 are done with
+            to_lds(vb, at.v, vtile(stage ^ 1));
+            at = locate(min(t + 2, full - 1));
+            to_lds(kb, at.k, ktile(stage));
+            fetch_pages(min(t + 3, full - 1));
+            raise(sc);
+            f32x4 next[RT][KTILES];
+            Weights p[RT][PX];
+            scores(ktile(stage ^ 1), next);
+            weigh(sc, p);
+            values(vtile(stage), p);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int x = 0; x < KTILES; ++x) sc[rt][x] = next[rt][x];
+            stage ^= 1;
+        }
+        arrive();
+        raise(sc);
+        Weights p[RT][PX];
+        weigh(sc, p);
+        values(vtile(stage), p);
     }
 
     // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
@@ -502,6 +618,7 @@ struct Worker {
     // Tiles [t0, t1) of the block: those of the prefix alone, the next one's loads under way while
     // one is computed, then the few that reach the tree's own rows, one after the other.
     __device__ __forceinline__ void run(int t0, int t1) {
+        fresh();
         const int c = tg % C::CPR;
         const int in_row = c * E < a.d ? c * 16 : 0;
         kbase = a.kp.p + (int64_t)h * a.kp.head + in_row;
@@ -512,23 +629,25 @@ struct Worker {
         const int full = min(t1, s.ctx / C::KW);
         int t = t0;
         if (t < full) {
-            int stage = 0;
-            fetch_pages(t);
-            load(t);
-            if (t + 1 < full) fetch_pages(t + 1);
-            store(0);
-            for (; t + 1 < full; ++t) {
-                load(t + 1);
-                fetch_pages(min(t + 2, full - 1));
-                if constexpr (C::WR > 1) __syncthreads();
-                compute<false>(t, stage);
-                if constexpr (C::STAGES > 1) stage ^= 1;
-                store(stage);
+            if constexpr (C::WR > 1) {
+                run_prefix(t, full);
+                t = full;
+            } else {
+                fetch_pages(t);
+                load(t);
+                if (t + 1 < full) fetch_pages(t + 1);
+                store(0);
+                for (; t + 1 < full; ++t) {
+                    load(t + 1);
+                    fetch_pages(min(t + 2, full - 1));
+                    compute<false>(t, 0);
+                    store(0);
+                }
+                compute<false>(t, 0);
+                ++t;
             }
-            if constexpr (C::WR > 1) __syncthreads();
-            compute<false>(t, stage);
-            ++t;
         }
+        fresh();
         for (; t < t1; ++t) {
             __syncthreads();
             if (threadIdx.x < C::WK) s_flag[threadIdx.x] = 0;
@@ -544,6 +663,7 @@ struct Worker {
     // Joins the waves that split the keys.  Afterwards wave wk holds the columns of its share in
     // acc[rt][0 .. DQ), and every wave has the rows' m and l.
     __device__ __forceinline__ void join_waves() {
+        fresh();
         const int c16 = lane & 15;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -620,6 +740,7 @@ struct Worker {
 
     // Rows of the block to o: acc[rt][0 .. DQ) / l.
     __device__ __forceinline__ void write(int block, bool poison) {
+        fresh();
         const int g = lane >> 4;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -649,21 +770,42 @@ struct Worker {
     __device__ __forceinline__ float* slot_ml(char* slot, int rt) const {
         return (float*)(slot + C::BM * C::D * 4) + ((wr * RT + rt) * 16 + (lane & 15)) * 2;
     }
+    // They pass between XCDs, whose L2 caches do not see each other's lines.  Their stores and
+    // loads are relaxed atomics of device scope, which go past these caches one by one; fences of
+    // that scope would write back and drop whole caches, once per wave (token steps of 64
+    // sequences over 128 keys: 70 us with fences).
+    static __device__ __forceinline__ void put(f32x4* p, f32x4 v) {
+        const uint64_t lo = __builtin_bit_cast(uint64_t, __builtin_shufflevector(v, v, 0, 1));
+        const uint64_t hi = __builtin_bit_cast(uint64_t, __builtin_shufflevector(v, v, 2, 3));
+        __hip_atomic_store((uint64_t*)p, lo, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store((uint64_t*)p + 1, hi, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    static __device__ __forceinline__ f32x2 get2(const void* p) {
+        return __builtin_bit_cast(
+            f32x2, __hip_atomic_load((const uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+    }
+    static __device__ __forceinline__ f32x4 get(const f32x4* p) {
+        return __builtin_shufflevector(get2(p), get2((const uint64_t*)p + 1), 0, 1, 2, 3);
+    }
     __device__ __forceinline__ void save(char* slot) const {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-            for (int dq = 0; dq < C::DQ; ++dq) *slot_acc(slot, rt, dq) = acc[rt][dq];
-            if (wk == 0 && lane < 16) {
-                float* ml = slot_ml(slot, rt);
-                ml[0] = m[rt];
-                ml[1] = l[rt];
-            }
+            for (int dq = 0; dq < C::DQ; ++dq) put(slot_acc(slot, rt, dq), acc[rt][dq]);
+            if (wk == 0 && lane < 16)
+                __hip_atomic_store((uint64_t*)slot_ml(slot, rt), __builtin_bit_cast(uint64_t, f32x2{m[rt], l[rt]}),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
+        // Stores that have returned are at the device's coherence point: what a thread does after
+        // the next barrier comes after them.
+        __builtin_amdgcn_s_waitcnt(0);
     }
     // Parts 0 .. n - 1 of a block, in the order of their keys; slot_of(i) is part i's place.
     template <class F>
     __device__ __forceinline__ void join_parts(int n, F slot_of) {
+        fresh();
+        // parts whose loads are in flight together: 32 registers of columns per thread or more
+        constexpr int U = RT * C::DQ >= 8 ? 1 : 8 / (RT * C::DQ);
         float top[RT], sum[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -672,18 +814,31 @@ struct Worker {
 #pragma unroll
             for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = zero4();
         }
-        for (int i = 0; i < n; ++i)
+        for (int i0 = 0; i0 < n; i0 += U) {
+            f32x2 ml[U][RT];
+            f32x4 x[U][RT][C::DQ];
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) top[rt] = fmaxf(top[rt], slot_ml(slot_of(i), rt)[0]);
-        for (int i = 0; i < n; ++i) {
-            char* slot = slot_of(i);
+            for (int u = 0; u < U; ++u) {
+                char* slot = slot_of(min(i0 + u, n - 1));
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const float* ml = slot_ml(slot, rt);
-                const float w = weight(ml[0], top[rt]);
-                sum[rt] += ml[1] * w;
+                for (int rt = 0; rt < RT; ++rt) {
+                    ml[u][rt] = get2(slot_ml(slot, rt));
 #pragma unroll
-                for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] += *slot_acc(slot, rt, dq) * w;
+                    for (int dq = 0; dq < C::DQ; ++dq) x[u][rt][dq] = get(slot_acc(slot, rt, dq));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u >= n) break;                 // its columns may be infinite: not even times zero
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const float next = fmaxf(top[rt], ml[u][rt][0]);
+                    const float w0 = weight(top[rt], next), w1 = weight(ml[u][rt][0], next);
+                    top[rt] = next;
+                    sum[rt] = sum[rt] * w0 + ml[u][rt][1] * w1;
+#pragma unroll
+                    for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = acc[rt][dq] * w0 + x[u][rt][dq] * w1;
+                }
             }
         }
 #pragma unroll
@@ -811,7 +966,6 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                         return plan.slots + ((c * plan.side + member) * 2 + (c == c0 ? 1 : 0)) * (int64_t)C::SLOT;
                     };
                     w.save(slot(cluster));
-                    __threadfence();
                     __syncthreads();
                     int32_t* arrived = plan.arrived + ((int64_t)b * a.Hk + w.h) * plan.max_blocks + block;
                     const int parts = (int)(c1 - c0) + 1;
@@ -819,7 +973,6 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                     __syncthreads();
                     out = s_last != 0;
                     if (out) {
-                        __threadfence();
                         w.join_parts(parts, [&](int i) { return slot(c0 + i); });
                         if (tid == 0) *arrived = 0;
                     }
