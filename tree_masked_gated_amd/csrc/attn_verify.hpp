@@ -17,9 +17,7 @@
 // packed weights are the second operand of O^T = V^T P^T as they are, provided that V's
 // operand lists its keys in the same order.  For bf16 that operand is read from LDS by the
 // transposing 64-bit read (four keys of one column per lane); for fp32 its elements are
-// single words.  The 16-byte pieces of a key's row are stored at piece c ^ swizzle(key), which
-// spreads both the rows of K (same piece, 16 keys) and the columns of V (four keys, four
-// pieces) over all banks.
+// single words.
 //
 // Work.  Tiles of all (sequence, key head, block of rows) form one line, cut into equal
 // shares, one per workgroup, so that contexts of very different lengths keep all CUs busy
@@ -62,7 +60,7 @@ struct Cfg {
     static constexpr int TG = 64 * WR;                  // threads that share keys
     static constexpr int NCH = KT * CPR / TG;           // pieces of K (and of V) per thread and step
     static constexpr int KSTEP = TG / CPR;              // keys between a thread's pieces
-    static constexpr int STAGES = WR == 1 ? 1 : 2;
+    static constexpr int STAGES = WR == 1 ? 1 : OCC == 1 && KT * WK * D * ES <= 16384 ? 3 : 2;
     static constexpr int ROWB = D * ES;
     static constexpr int TILEB = KT * ROWB;
     static constexpr int LDS = STAGES * WK * 2 * TILEB;
@@ -85,14 +83,24 @@ struct Plan {
     char* slots;       // [grid][2][SLOT]
 };
 
+// The place of piece c of a key's row is c ^ swizzle(key).  LDS serves a wave's 16-byte reads of
+// K in groups of 16 lanes, keys 0-3 and 12-15 of one piece together with keys 4-11 of the piece
+// next to it, and the transposing reads of V in halves, keys 0-7 (8-15) of two neighbouring
+// pieces; each must meet all banks once.  For the first the place's lowest bit must not tell
+// keys 0-3 and 12-15 from the others, for the second the other bits must tell keys 0-7 apart (and
+// 8-15).  fp32 reads V as words of keys 4 g + i of four neighbouring pieces: there the high bits
+// tell the g apart.
 template <class C>
 __device__ __forceinline__ int swizzle(int key) {
-    if constexpr (C::IO == GDN_F32)
+    if constexpr (C::IO == GDN_F32) {
         return (((key >> 2) & 3) << 2) | (key & 3);
-    else if constexpr (C::CPR == 8)
-        return (((key >> 1) & 1) << 2) | ((key >> 2) & 3);
-    else
-        return ((key & 3) << 2) | ((key >> 2) & 3);
+    } else if constexpr (C::CPR == 8) {      // two keys meet the banks side by side
+        const int k = (key >> 1) & 7;
+        return (((k & 3) ^ ((k >> 2) << 1)) << 1) | (k >> 2);
+    } else {
+        const int k = key & 15;
+        return (((k & 7) ^ ((k >> 3) << 2)) << 1) | (k >> 3);
+    }
 }
 
 // Sequence b: its rows, prefix and share of the work.
@@ -523,54 +531,70 @@ struct Worker {
                              :: "s"(to + i * C::TG * 16), "v"(from) : "memory");
         }
     }
-    // What this wave sent to LDS has arrived, and so has every other wave's.
+    // All but the newest `later` pieces that each thread sent to LDS have arrived, for every wave.
+    template <int later>
     static __device__ __forceinline__ void arrive() {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(later) : "memory");
         __syncthreads();
     }
+    // Tiles [t0, full).  While the values of tile t are added, the scores of t + 1 are formed: both
+    // products and the exponentials between them are independent and fill each other's gaps.
+    // Slot t % STAGES of LDS holds K of t until these scores, V of t until these values are done.
     __device__ __forceinline__ void run_prefix(int t0, int full) {
+        constexpr int S = C::STAGES;
         if (a.d < C::D) {
             for (int i = threadIdx.x; i < C::LDS / 16; i += C::NT) ((uint4*)lds)[i] = uint4{0, 0, 0, 0};
             __syncthreads();
         }
         const char* kb = a.kp.p + (int64_t)h * a.kp.head;
         const char* vb = a.vp.p + (int64_t)h * a.vp.head;
+        const int last = full - 1;
         fetch_pages(t0);
         Ahead at = locate(t0);
         to_lds(kb, at.k, ktile(0));
-        to_lds(vb, at.v, vtile(0));
-        fetch_pages(min(t0 + 1, full - 1));
-        at = locate(min(t0 + 1, full - 1));
-        fetch_pages(min(t0 + 2, full - 1));
+#pragma unroll
+        for (int i = 1; i < S; ++i) {
+            fetch_pages(min(t0 + i, last));
+            to_lds(vb, at.v, vtile(i - 1));
+            at = locate(min(t0 + i, last));
+            to_lds(kb, at.k, ktile(i));
+        }
+        fetch_pages(min(t0 + S, last));
+        arrive<0>();
         f32x4 sc[RT][KTILES];
-        arrive();
-        to_lds(kb, at.k, ktile(1));
         scores(ktile(0), sc);
-        int stage = 0;
-        for (int t = t0; t + 1 < full; ++t) {
-            arrive();
-            // K of t + 1 and V of t are there; K of t and V of t - 1 are done with
-            to_lds(vb, at.v, vtile(stage ^ 1));
-            at = locate(min(t + 2, full - 1));
-            to_lds(kb, at.k, ktile(stage));
-            fetch_pages(min(t + 3, full - 1));
+        int here = 0, next = 1, prev = S - 1;    // slots of t, t + 1 and t - 1
+        for (int t = t0; t < last; ++t) {
+            // K of t + 1 and V of t are needed; K of t and V of t - 1 are done with.  Fewer pieces
+            // are under way near the end, and where rows have ended not every wave has some.
+            if (S == 2 || t + S > last || t == t0 || a.d < C::D)
+                arrive<0>();
+            else
+                arrive<(S - 2) * 2 * NCH>();
+            const Ahead old = at;
+            at = locate(min(t + S, last));
+            fetch_pages(min(t + S + 1, last));
+            if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
+            if (t + S < full) to_lds(kb, at.k, ktile(here));
             raise(sc);
-            f32x4 next[RT][KTILES];
+            f32x4 sc1[RT][KTILES];
             Weights p[RT][PX];
-            scores(ktile(stage ^ 1), next);
+            scores(ktile(next), sc1);
             weigh(sc, p);
-            values(vtile(stage), p);
+            values(vtile(here), p);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int x = 0; x < KTILES; ++x) sc[rt][x] = next[rt][x];
-            stage ^= 1;
+                for (int x = 0; x < KTILES; ++x) sc[rt][x] = sc1[rt][x];
+            prev = here;
+            here = next;
+            next = next + 1 == S ? 0 : next + 1;
         }
-        arrive();
+        arrive<0>();
         raise(sc);
         Weights p[RT][PX];
         weigh(sc, p);
-        values(vtile(stage), p);
+        values(vtile(here), p);
     }
 
     // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
