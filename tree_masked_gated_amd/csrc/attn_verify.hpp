@@ -466,6 +466,45 @@ struct Worker {
         }
     }
 
+    // values() and the next tile's scores() as one run of 2 RT products per LDS fragment: the
+    // fragments 0 .. kPv - 1 are those of V, the others those of K.
+    static constexpr int kPv = KTILES / 2 * DT, kFrags = kPv + KTILES * (C::CPR / 4);
+    static constexpr int kEarly = 6;         // fragments read ahead: their latency in products
+    __device__ __forceinline__ bf16x8 fragment(int u, const char* vt, const char* kt) const {
+        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+        const int g = lane >> 4, c16 = lane & 15;
+        if (u < kPv) {
+            // lane (row of the read c16 / 4, columns 4 (c16 % 4) ..): keys 4g + c16 / 4 of both halves
+            const int key = 4 * g + (c16 >> 2), c = u % DT * 2 + ((c16 >> 1) & 1);
+            const char* at = vt + (u / DT * 32 + key) * C::ROWB + (c16 & 1) * 8 + (c ^ swizzle<C>(key)) * 16;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 16 * C::ROWB));
+            return __builtin_shufflevector(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi), 0, 1, 2,
+                                           3, 4, 5, 6, 7);
+        }
+        const int x = (u - kPv) / (C::CPR / 4), ks = (u - kPv) % (C::CPR / 4);
+        return *(const bf16x8*)(kt + (x * 16 + c16) * C::ROWB + ((ks * 4 + g) ^ swizzle<C>(c16)) * 16);
+    }
+    __device__ __forceinline__ void products(const char* vt, const char* kt, const Weights (&p)[RT][PX],
+                                             bf16x8 (&f)[kFrags], f32x4 (&sc)[RT][KTILES]) {
+#pragma unroll
+        for (int u = 0; u < kFrags; ++u) {
+            if (u + kEarly < kFrags) f[u + kEarly] = fragment(u + kEarly, vt, kt);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                if (u < kPv) {
+                    f32x4& to = acc[rt][u % DT];
+                    to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u], p[rt][u / DT], to, 0, 0, 0);
+                } else {
+                    const int x = (u - kPv) / (C::CPR / 4), ks = (u - kPv) % (C::CPR / 4);
+                    if (ks == 0) sc[rt][x] = zero4();
+                    sc[rt][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u], q[rt][ks], sc[rt][x], 0, 0, 0);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
     // A tile in LDS, all at once.
     template <bool MIXED>
     __device__ __forceinline__ void compute(int t, int stage) {
@@ -537,6 +576,15 @@ struct Worker {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(later) : "memory");
         __syncthreads();
     }
+    // A barrier between the halves of a tile.  This wave's reads of LDS have returned; what it has
+    // under way to LDS is waited for elsewhere.
+    static __device__ __forceinline__ void turn() {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
     // Tiles [t0, full).  While the values of tile t are added, the scores of t + 1 are formed: both
     // products and the exponentials between them are independent and fill each other's gaps.
     // Slot t % STAGES of LDS holds K of t until these scores, V of t until these values are done.
@@ -564,37 +612,81 @@ struct Worker {
         f32x4 sc[RT][KTILES];
         scores(ktile(0), sc);
         int here = 0, next = 1, prev = S - 1;    // slots of t, t + 1 and t - 1
-        for (int t = t0; t < last; ++t) {
-            // K of t + 1 and V of t are needed; K of t and V of t - 1 are done with.  Fewer pieces
-            // are under way near the end, and where rows have ended not every wave has some.
-            if (S == 2 || t + S > last || t == t0 || a.d < C::D)
-                arrive<0>();
-            else
-                arrive<(S - 2) * 2 * NCH>();
-            const Ahead old = at;
-            at = locate(min(t + S, last));
-            fetch_pages(min(t + S + 1, last));
-            if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
-            if (t + S < full) to_lds(kb, at.k, ktile(here));
+        if constexpr (C::WR == 8) {
+            // Two waves share a SIMD.  The second four run half a tile behind the first, so that one
+            // of the two has matrix work while the other forms weights; a barrier after each half
+            // keeps them so.  Per tile: weights(t) | values(t), scores(t + 1) |.  The slots that a
+            // wave's second half reads are filled when any wave's previous second half ends, and
+            // both groups are done with those of t - 1 when any wave's second half of t begins.
+            static_assert(S == 3, "slots");
+            if (wr >= 4) turn();
+            for (int t = t0; t < last; ++t) {
+                bf16x8 f[kFrags];
+#pragma unroll
+                for (int u = 0; u < kEarly; ++u) f[u] = fragment(u, vtile(here), ktile(next));
+                raise(sc);
+                Weights p[RT][PX];
+                weigh(sc, p);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int x = 0; x < PX; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
+                turn();
+                const Ahead old = at;
+                at = locate(min(t + S, last));
+                fetch_pages(min(t + S + 1, last));
+                if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
+                if (t + S < full) to_lds(kb, at.k, ktile(here));
+                __builtin_amdgcn_s_setprio(1);
+                products(vtile(here), ktile(next), p, f, sc);
+                __builtin_amdgcn_s_setprio(0);
+                if (t + S >= full || a.d < C::D)
+                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                else
+                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NCH) : "memory");
+                turn();
+                prev = here;
+                here = next;
+                next = next + 1 == S ? 0 : next + 1;
+            }
+            if (wr < 4) turn();
             raise(sc);
-            f32x4 sc1[RT][KTILES];
             Weights p[RT][PX];
-            scores(ktile(next), sc1);
             weigh(sc, p);
             values(vtile(here), p);
+        } else {
+            for (int t = t0; t < last; ++t) {
+                // K of t + 1 and V of t are needed; K of t and V of t - 1 are done with.  Fewer pieces
+                // are under way near the end, and where rows have ended not every wave has some.
+                if (S == 2 || t + S > last || t == t0 || a.d < C::D)
+                    arrive<0>();
+                else
+                    arrive<(S - 2) * 2 * NCH>();
+                const Ahead old = at;
+                at = locate(min(t + S, last));
+                fetch_pages(min(t + S + 1, last));
+                if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
+                if (t + S < full) to_lds(kb, at.k, ktile(here));
+                raise(sc);
+                f32x4 sc1[RT][KTILES];
+                Weights p[RT][PX];
+                scores(ktile(next), sc1);
+                weigh(sc, p);
+                values(vtile(here), p);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
+                for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int x = 0; x < KTILES; ++x) sc[rt][x] = sc1[rt][x];
-            prev = here;
-            here = next;
-            next = next + 1 == S ? 0 : next + 1;
+                    for (int x = 0; x < KTILES; ++x) sc[rt][x] = sc1[rt][x];
+                prev = here;
+                here = next;
+                next = next + 1 == S ? 0 : next + 1;
+            }
+            arrive<0>();
+            raise(sc);
+            Weights p[RT][PX];
+            weigh(sc, p);
+            values(vtile(here), p);
         }
-        arrive<0>();
-        raise(sc);
-        Weights p[RT][PX];
-        weigh(sc, p);
-        values(vtile(here), p);
     }
 
     // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
