@@ -482,7 +482,7 @@ struct Worker {
             return __builtin_shufflevector(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi), 0, 1, 2,
                                            3, 4, 5, 6, 7);
         }
-        const int x = (u - kPv) / (C::CPR / 4), ks = (u - kPv) % (C::CPR / 4);
+        const int x = (u - kPv) % KTILES, ks = (u - kPv) / KTILES;
         return *(const bf16x8*)(kt + (x * 16 + c16) * C::ROWB + ((ks * 4 + g) ^ swizzle<C>(c16)) * 16);
     }
     __device__ __forceinline__ void products(const char* vt, const char* kt, const Weights (&p)[RT][PX],
@@ -496,12 +496,12 @@ struct Worker {
                     f32x4& to = acc[rt][u % DT];
                     to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u], p[rt][u / DT], to, 0, 0, 0);
                 } else {
-                    const int x = (u - kPv) / (C::CPR / 4), ks = (u - kPv) % (C::CPR / 4);
+                    const int x = (u - kPv) % KTILES, ks = (u - kPv) / KTILES;
                     if (ks == 0) sc[rt][x] = zero4();
                     sc[rt][x] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u], q[rt][ks], sc[rt][x], 0, 0, 0);
                 }
             }
-            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0x6);     // only addresses may move
         }
     }
 
@@ -545,15 +545,16 @@ struct Worker {
     __device__ __forceinline__ int piece_at(int i) const {
         return (tg % C::CPR) ^ swizzle<C>(tg / C::CPR + i * C::KSTEP);
     }
-    __device__ __forceinline__ Ahead locate(int t) {
+    __device__ __forceinline__ Ahead locate(int t) { return locate(t, pid); }
+    __device__ __forceinline__ Ahead locate(int t, const int (&ids)[NCH]) {
         const int j0 = key0(t) + tg / C::CPR;
         Ahead at;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const uint32_t j = j0 + i * C::KSTEP;
             const uint32_t r = j - quot(a.page, j) * a.page.d;
-            top_page = max(top_page, (uint32_t)pid[i]);
-            const uint32_t id = min((uint32_t)pid[i], (uint32_t)a.n_pages - 1u);
+            top_page = max(top_page, (uint32_t)ids[i]);
+            const uint32_t id = min((uint32_t)ids[i], (uint32_t)a.n_pages - 1u);
             at.k[i] = offset16(a.kp, id, r) + piece_at(i);
             at.v[i] = offset16(a.vp, id, r) + piece_at(i);
         }
@@ -619,6 +620,9 @@ struct Worker {
             // wave's second half reads are filled when any wave's previous second half ends, and
             // both groups are done with those of t - 1 when any wave's second half of t begins.
             static_assert(S == 3, "slots");
+            Ahead old = at;
+            at = locate(min(t0 + S, last));
+            fetch_pages(min(t0 + S + 1, last));
             if (wr >= 4) turn();
             for (int t = t0; t < last; ++t) {
                 bf16x8 f[kFrags];
@@ -632,11 +636,14 @@ struct Worker {
 #pragma unroll
                     for (int x = 0; x < PX; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
                 turn();
-                const Ahead old = at;
-                at = locate(min(t + S, last));
-                fetch_pages(min(t + S + 1, last));
+                int ids[NCH];
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) ids[i] = pid[i];
+                fetch_pages(min(t + S + 2, last));
                 if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
                 if (t + S < full) to_lds(kb, at.k, ktile(here));
+                old = at;
+                at = locate(min(t + S + 1, last), ids);
                 __builtin_amdgcn_s_setprio(1);
                 products(vtile(here), ktile(next), p, f, sc);
                 __builtin_amdgcn_s_setprio(0);
