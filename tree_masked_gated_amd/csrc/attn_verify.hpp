@@ -68,6 +68,11 @@ struct Cfg {
     static constexpr int DQ = DT / WK;                  // of these, a wave's share at the end
     static constexpr int KTILES = KT / 16;
     static constexpr int SLOT = BM * (D + 2) * 4;       // bytes of a partial result
+    // The last part of a block stays in registers where a thread's share of it is large (256 rows:
+    // 131 KB that are neither written nor read); small ones take one way only.
+    static constexpr bool KEEP = RT * DQ >= 16;
+    // Time to join one part, in tiles (measured with one sequence; the parts are as large as the rows).
+    static constexpr float PART = IO == GDN_F32 || WR == 1 ? 0.05f : 1.0f;
     static_assert(LDS + 4096 <= kMaxLds, "LDS of a workgroup");
     static_assert(TG % CPR == 0 && NCH >= 1, "a thread keeps its piece of the row");
     static_assert(KT % 32 == 0 && DT % WK == 0, "mask words, columns of the joining waves");
@@ -469,7 +474,7 @@ struct Worker {
     // values() and the next tile's scores() as one run of 2 RT products per LDS fragment: the
     // fragments 0 .. kPv - 1 are those of V, the others those of K.
     static constexpr int kPv = KTILES / 2 * DT, kFrags = kPv + KTILES * (C::CPR / 4);
-    static constexpr int kEarly = 6;         // fragments read ahead: their latency in products
+    static constexpr int kEarly = 5;         // fragments read ahead: their latency in products
     __device__ __forceinline__ bf16x8 fragment(int u, const char* vt, const char* kt) const {
         typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
         const int g = lane >> 4, c16 = lane & 15;
@@ -923,49 +928,53 @@ struct Worker {
         // the next barrier comes after them.
         __builtin_amdgcn_s_waitcnt(0);
     }
-    // Parts 0 .. n - 1 of a block, in the order of their keys; slot_of(i) is part i's place.
+    // Parts 0 .. n - 1 of a block, in the order of their keys; slot_of(i) is part i's place.  With
+    // KEEP part `mine` is in this workgroup's registers.
     template <class F>
-    __device__ __forceinline__ void join_parts(int n, F slot_of) {
+    __device__ __forceinline__ void join_parts(int n, int mine, F slot_of) {
         fresh();
-        // parts whose loads are in flight together: 32 registers of columns per thread or more
-        constexpr int U = RT * C::DQ >= 8 ? 1 : 8 / (RT * C::DQ);
-        float top[RT], sum[RT];
+        // parts whose loads are in flight together
+        constexpr int U = C::DQ >= 8 ? 1 : 8 / C::DQ;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            top[rt] = -INFINITY;
-            sum[rt] = 0.f;
+            const f32x2 own_ml = f32x2{m[rt], l[rt]};
+            f32x4 own[C::DQ];
+            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-            for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = zero4();
-        }
-        for (int i0 = 0; i0 < n; i0 += U) {
-            f32x2 ml[U][RT];
-            f32x4 x[U][RT][C::DQ];
+            for (int dq = 0; dq < C::DQ; ++dq) {
+                own[dq] = acc[rt][dq];
+                acc[rt][dq] = zero4();
+            }
+            for (int i0 = 0; i0 < n; i0 += U) {
+                f32x2 ml[U];
+                f32x4 x[U][C::DQ];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                char* slot = slot_of(min(i0 + u, n - 1));
+                for (int u = 0; u < U; ++u) {
+                    const int i = min(i0 + u, n - 1);
+                    if (C::KEEP && i == mine) {
+                        ml[u] = own_ml;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    ml[u][rt] = get2(slot_ml(slot, rt));
+                        for (int dq = 0; dq < C::DQ; ++dq) x[u][dq] = own[dq];
+                        continue;
+                    }
+                    char* slot = slot_of(i);
+                    ml[u] = get2(slot_ml(slot, rt));
 #pragma unroll
-                    for (int dq = 0; dq < C::DQ; ++dq) x[u][rt][dq] = get(slot_acc(slot, rt, dq));
+                    for (int dq = 0; dq < C::DQ; ++dq) x[u][dq] = get(slot_acc(slot, rt, dq));
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (i0 + u >= n) break;             // its columns may be infinite: not even times zero
+                    const float next = fmaxf(top, ml[u][0]);
+                    const float w0 = weight(top, next), w1 = weight(ml[u][0], next);
+                    top = next;
+                    sum = sum * w0 + ml[u][1] * w1;
+#pragma unroll
+                    for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = acc[rt][dq] * w0 + x[u][dq] * w1;
                 }
             }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u >= n) break;                 // its columns may be infinite: not even times zero
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const float next = fmaxf(top[rt], ml[u][rt][0]);
-                    const float w0 = weight(top[rt], next), w1 = weight(ml[u][rt][0], next);
-                    top[rt] = next;
-                    sum[rt] = sum[rt] * w0 + ml[u][rt][1] * w1;
-#pragma unroll
-                    for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = acc[rt][dq] * w0 + x[u][rt][dq] * w1;
-                }
-            }
+            l[rt] = sum;
         }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) l[rt] = sum[rt];
     }
 };
 
@@ -1014,8 +1023,10 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
         s_pre[tid] = base + x;               // kept where one round covers the batch
         __syncthreads();
     }
-    const int64_t share = max((total + plan.clusters - 1) / plan.clusters,
-                              (int64_t)((longest + kMaxParts - 2) / (kMaxParts - 1)));
+    // Shares of a block of n tiles in shares of s take s tiles' time and then n / s parts' to join;
+    // a workgroup that would otherwise idle is not worth a part below s = sqrt(n PART).
+    const int least = max((longest + kMaxParts - 2) / (kMaxParts - 1), (int)__fsqrt_rn((float)longest * C::PART));
+    const int64_t share = max((total + plan.clusters - 1) / plan.clusters, (int64_t)least);
     int64_t at = cluster * share;
     const int64_t end = min(total, at + share);
     if (at >= end) return;
@@ -1088,15 +1099,24 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                     auto slot = [&](int64_t c) {
                         return plan.slots + ((c * plan.side + member) * 2 + (c == c0 ? 1 : 0)) * (int64_t)C::SLOT;
                     };
-                    w.save(slot(cluster));
-                    __syncthreads();
                     int32_t* arrived = plan.arrived + ((int64_t)b * a.Hk + w.h) * plan.max_blocks + block;
                     const int parts = (int)(c1 - c0) + 1;
-                    if (tid == 0) s_last = atomicAdd(arrived, 1) == parts - 1;
-                    __syncthreads();
-                    out = s_last != 0;
+                    // Where all others have arrived, this part stays in registers.
+                    if constexpr (C::KEEP) {
+                        if (tid == 0)
+                            s_last = __hip_atomic_load(arrived, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+                        __syncthreads();
+                        out = s_last != 0;
+                    }
+                    if (!out) {
+                        w.save(slot(cluster));
+                        __syncthreads();
+                        if (tid == 0) s_last = atomicAdd(arrived, 1) == parts - 1;
+                        __syncthreads();
+                        out = s_last != 0;
+                    }
                     if (out) {
-                        w.join_parts(parts, [&](int i) { return slot(c0 + i); });
+                        w.join_parts(parts, (int)(cluster - c0), [&](int i) { return slot(c0 + i); });
                         if (tid == 0) *arrived = 0;
                     }
                 }
@@ -1146,7 +1166,7 @@ inline hipError_t launch_cfg(const AttnArgs& a, hipStream_t stream) {
 // to registers to LDS, without a barrier.  Many rows: the waves split the rows and share
 // each tile.
 template <int IO, int D, class F>
-inline auto choose(int rows, F f) {
+inline auto choose(int rows, int units, F f) {
     if constexpr (IO == GDN_F32) {
         // 256 columns of fp32 for four waves' own keys would not fit the LDS
         if constexpr (D <= 128) {
@@ -1155,13 +1175,13 @@ inline auto choose(int rows, F f) {
         return f(Cfg<IO, D, 1, 4, 1, 32, (D <= 128 ? 2 : 1)>{});
     } else {
         constexpr int occ = D <= 128 ? 2 : 1;
+        auto few = [&](int bm) { return (int64_t)units * ((rows + bm - 1) / bm) < kCUs / 2; };
         if (rows <= 16) return f(Cfg<IO, D, 1, 1, 4, 32, occ>{});
-        if (rows <= 32) return f(Cfg<IO, D, 2, 1, 4, 32, occ>{});
-        if (rows <= 64) return f(Cfg<IO, D, 2, 2, 2, 32, occ>{});
+        if (rows <= 64 || few(128)) return f(Cfg<IO, D, 2, 2, 2, 32, occ>{});
         if constexpr (D > 128) {
             return f(Cfg<IO, D, 2, 4, 1, 32, 1>{});
         } else {
-            if (rows <= 128) return f(Cfg<IO, D, 2, 4, 1, 64, 2>{});
+            if (rows <= 128 || few(256)) return f(Cfg<IO, D, 2, 4, 1, 64, 2>{});
             return f(Cfg<IO, D, 2, 8, 1, 64, 1>{});
         }
     }
@@ -1169,11 +1189,11 @@ inline auto choose(int rows, F f) {
 
 template <int IO, int D>
 inline hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
-    return choose<IO, D>(a.N * a.group, [&](auto c) { return launch_cfg<decltype(c)>(a, stream); });
+    return choose<IO, D>(a.N * a.group, a.B * a.Hk, [&](auto c) { return launch_cfg<decltype(c)>(a, stream); });
 }
 template <int IO, int D>
 inline size_t bytes_d(int B, int N, int group, int Hk) {
-    return choose<IO, D>(N * group, [&](auto c) { return plan_bytes<decltype(c)>(B, N, group, Hk); });
+    return choose<IO, D>(N * group, B * Hk, [&](auto c) { return plan_bytes<decltype(c)>(B, N, group, Hk); });
 }
 
 }  // namespace attn
