@@ -74,33 +74,28 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
 
 // ------------------------------------------------------------------ copy
 
-// Pages that are one dense run of bytes in memory (rows first or heads first), in chunks of
-// kThreads * kCopyUnroll 16-byte pieces.
-constexpr int kCopyUnroll = 4;
+// Pages that are one dense run of bytes in memory (rows first or heads first), 4 KB to a workgroup,
+// one 16-byte piece to a thread; pool by pool and layer by layer, so that all that runs at a time
+// lies in one of them.  Bound by memory (2500 pages of 4 layers, 32 KB each: 3.6 TB/s read and
+// written; longer loops per workgroup and pages outermost were slower, 468 us for 369, and stores
+// that the L2 keeps 405).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+constexpr int kCopyGrid = 1 << 20;
 template <int ES>
-__global__ __launch_bounds__(kThreads) void copy_dense_kernel(CopyArgs a, int chunks, int bytes) {
-    const int n = min(*a.count, a.n);
-    const int64_t total = (int64_t)n * a.n_layers * 2 * chunks;
-    for (int64_t w = blockIdx.x; w < total; w += gridDim.x) {
-        const int chunk = (int)(w % chunks);
-        int64_t x = w / chunks;
-        const int kv = (int)(x & 1);
-        x >>= 1;
-        const int layer = (int)(x % a.n_layers), i = (int)(x / a.n_layers);
+__global__ __launch_bounds__(kThreads) void copy_dense_kernel(CopyArgs a, FastDiv chunks, int bytes) {
+    const uint32_t n = (uint32_t)max(min(*a.count, a.n), 0);
+    const uint32_t run = n * chunks.d, total = run * 2 * (uint32_t)a.n_layers;
+    for (uint32_t w = blockIdx.x; w < total; w += gridDim.x) {
+        const uint32_t part = w / run, y = w - part * run;
+        const uint32_t i = quot(chunks, y), chunk = y - i * chunks.d;
         const int s = a.src[i], t = a.dst[i];
-        if (!is_page(s, a.n_pages) || !is_page(t, a.n_pages)) continue;
-        const Pool& pool = kv ? a.vp : a.kp;
-        char* base = pool.p + (int64_t)layer * (kv ? a.v_layer : a.k_layer) * ES;
-        const char* from = base + (int64_t)s * pool.page * ES;
-        char* to = base + (int64_t)t * pool.page * ES;
-        uint4 r[kCopyUnroll];
-        const int at = (chunk * kThreads * kCopyUnroll + (int)threadIdx.x) * 16;
-#pragma unroll
-        for (int u = 0; u < kCopyUnroll; ++u)
-            if (at + u * kThreads * 16 < bytes) r[u] = *(const uint4*)(from + at + u * kThreads * 16);
-#pragma unroll
-        for (int u = 0; u < kCopyUnroll; ++u)
-            if (at + u * kThreads * 16 < bytes) *(uint4*)(to + at + u * kThreads * 16) = r[u];
+        const int at = ((int)chunk * kThreads + (int)threadIdx.x) * 16;
+        if (!is_page(s, a.n_pages) || !is_page(t, a.n_pages) || at >= bytes) continue;
+        const int64_t layer = part >> 1;
+        const Pool& pool = part & 1 ? a.vp : a.kp;
+        char* base = pool.p + layer * (part & 1 ? a.v_layer : a.k_layer) * ES + at;
+        const u32x4 x = *(const u32x4*)(base + s * pool.page * ES);
+        __builtin_nontemporal_store(x, (u32x4*)(base + t * pool.page * ES));
     }
 }
 
@@ -229,6 +224,7 @@ __global__ __launch_bounds__(kOne) void reserve_kernel(PageArgs a, const int32_t
     __shared__ int64_t s_first[kMaxSlots + 1];
     __shared__ int64_t s_part[kOne / 64];
     __shared__ int s_cpart[kOne / 64];
+    __shared__ uint16_t s_free[kOne * kScan];
     extern __shared__ int s_hash[];          // key, askers, last asker: buckets each
     int* key = s_hash;
     int* askers = s_hash + buckets;
@@ -322,51 +318,54 @@ __global__ __launch_bounds__(kOne) void reserve_kernel(PageArgs a, const int32_t
     for (int o = 1; o < 64; o <<= 1) top = max(top, (int64_t)__shfl_xor(top, o));
     __syncthreads();
     if ((tid & 63) == 0) s_part[tid >> 6] = top;
-    // the hash table is done with: per slot, where its copy goes in the list, or -1
+    // the hash table is done with: per slot, where its copy goes in the list (or -1), the column of
+    // its last page and that of its first missing one
     int* copy_at = s_hash;
+    int* tail_col = s_hash + S;
+    int* next_col = s_hash + 2 * S;
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
         const int s = tid * kPer + u;
         if (s >= S) continue;
         copy_at[s] = copies[u] ? at_copy++ : -1;
+        tail_col[s] = len[u] / a.page_rows;
+        next_col[s] = held[u];
         if (good[u]) a.held[s] = max((int)want[u], held[u]);
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kOne / 64; ++w) top = max(top, s_part[w]);
-    // 4. hand the pages out
+    // 4. hand the pages out: the free ones of a round are listed by rank, a thread takes a rank
     int64_t base = 0;
     for (int p0 = 0; p0 < a.n_pages && base < top; p0 += kOne * kScan) {
         uint32_t bits = scan_pages(a.ref, p0 + tid * kScan, a.n_pages, true);
         int total;
-        int64_t f = base + block_exclusive<int>(__popc(bits), s_cpart, total);
-        while (bits && f < top) {
-            const int p = p0 + tid * kScan + __ffs(bits) - 1;
-            bits &= bits - 1;
-            int lo = 0, hi = kMaxSlots;      // first[lo] <= f < first[hi]
+        int at = block_exclusive<int>(__popc(bits), s_cpart, total);
+        for (; bits; bits &= bits - 1) s_free[at++] = (uint16_t)(tid * kScan + __ffs(bits) - 1);
+        __syncthreads();
+        const int take = (int)min((int64_t)total, top - base);
+        for (int x = tid; x < take; x += kOne) {
+            const int p = p0 + s_free[x];
+            const int64_t f = base + x;
+            int lo = 0, hi = S;              // first[lo] <= f < first[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
                 if (s_first[mid] <= f) lo = mid; else hi = mid;
             }
             const int s = lo;
-            int off = (int)(f - s_first[s]);
+            const int off = (int)(f - s_first[s]);
             const int c = copy_at[s];
             a.ref[p] = 1;
             if (c >= 0 && off == 0) {
-                int32_t* e = &a.table[(int64_t)s * a.width + a.length[s] / a.page_rows];
-                src[c] = *e;
+                int32_t* e = &a.table[(int64_t)s * a.width + tail_col[s]];
+                const int old = *e;
+                src[c] = old;
                 dst[c] = p;
-                atomicSub(&a.ref[*e], 1);
+                atomicSub(&a.ref[old], 1);
                 *e = p;
             } else {
-                off -= c >= 0 ? 1 : 0;
-                // the first page that was missing is column held (before this call)
-                const int need_rows = need[s];
-                const int64_t w = ((int64_t)a.length[s] + need_rows + a.page_rows - 1) / a.page_rows;
-                const int64_t fresh = s_first[s + 1] - s_first[s] - (c >= 0 ? 1 : 0);
-                a.table[(int64_t)s * a.width + (w - fresh) + off] = p;
+                a.table[(int64_t)s * a.width + next_col[s] + off - (c >= 0 ? 1 : 0)] = p;
             }
-            ++f;
         }
         base += total;
     }
@@ -452,14 +451,12 @@ hipError_t launch_append(const AppendArgs& a, int io, hipStream_t stream) {
 hipError_t launch_pages_copy(const CopyArgs& a, int io, hipStream_t stream) {
     const int es = io == GDN_F32 ? 4 : 2;
     const int64_t parts = (int64_t)a.n * a.n_layers * 2;
-    if (dense(a.kp, a.page_rows, a.Hk, a.d) && dense(a.vp, a.page_rows, a.Hk, a.d) &&
-        (int64_t)a.page_rows * a.Hk * a.d * es < (1 << 30)) {
-        const int bytes = a.page_rows * a.Hk * a.d * es;
-        const int chunk = kThreads * kCopyUnroll * 16;
-        const int chunks = (bytes + chunk - 1) / chunk;
-        const unsigned grid = (unsigned)std::min<int64_t>(parts * chunks, 256 * 8);
+    const int64_t bytes = (int64_t)a.page_rows * a.Hk * a.d * es, chunks = (bytes + kThreads * 16 - 1) / (kThreads * 16);
+    if (dense(a.kp, a.page_rows, a.Hk, a.d) && dense(a.vp, a.page_rows, a.Hk, a.d) && bytes < (1 << 30) &&
+        parts * chunks + kCopyGrid < 0xffffffffLL && (int64_t)a.n * chunks < (1LL << 31)) {
+        const unsigned grid = (unsigned)std::min<int64_t>(parts * chunks, kCopyGrid);
         return launch(es == 4 ? copy_dense_kernel<4> : copy_dense_kernel<2>, dim3(grid), dim3(kThreads), 0, stream, a,
-                      chunks, bytes);
+                      fast_div((uint32_t)chunks), (int)bytes);
     }
     const unsigned grid = (unsigned)std::min<int64_t>(parts, 256 * 8);
     return launch(es == 4 ? copy_strided_kernel<4> : copy_strided_kernel<2>, dim3(grid), dim3(kThreads), 0, stream, a);
