@@ -407,7 +407,7 @@ struct Worker {
                     l[rt] += (sc[rt][x][0] + sc[rt][x][1]) + (sc[rt][x][2] + sc[rt][x][3]);
                 }
             } else {
-                // The weights are rounded to bf16, 2^-9 of each: the product needs two bf16
+                // The weights are rounded to bf16, 2^-8 of each at most: the product needs two bf16
                 // operands.  l sums the rounded ones, so that the weights' quotients add up to one
                 // and a row that sees one key gets that key's value exactly.
                 const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
