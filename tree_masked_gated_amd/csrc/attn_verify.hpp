@@ -71,8 +71,14 @@ struct Cfg {
     // The last part of a block stays in registers where a thread's share of it is large (256 rows:
     // 131 KB that are neither written nor read); small ones take one way only.
     static constexpr bool KEEP = RT * DQ >= 16;
-    // Time to join one part, in tiles (measured with one sequence; the parts are as large as the rows).
+    // Time that one more part takes to join, in tiles (measured with one sequence).
     static constexpr float PART = IO == GDN_F32 || WR == 1 ? 0.05f : 1.0f;
+    // Parts that one workgroup joins.  A token's are small and many: groups of them are joined side by
+    // side, then their results (one token over 4k and 32k keys: 23.5 and 46.5 us without groups, 19.8
+    // and 40.0 with).  Parts of many rows are few, and a second step costs more than it saves there
+    // (one tree of 128 rows over 4k keys: 39 us without, 43 with).
+    static constexpr int GROUP = WR == 1 ? 8 : kMaxParts;
+    static constexpr int COUNTERS = GROUP < kMaxParts ? 1 + kMaxParts / GROUP : 1;
     static_assert(LDS + 4096 <= kMaxLds, "LDS of a workgroup");
     static_assert(TG % CPR == 0 && NCH >= 1, "a thread keeps its piece of the row");
     static_assert(KT % 32 == 0 && DT % WK == 0, "mask words, columns of the joining waves");
@@ -84,7 +90,7 @@ struct Plan {
     int side;          // C: workgroups that take neighbouring blocks of rows over the same keys
     int clusters;      // grid / C
     int max_blocks;    // blocks of rows of the largest tree
-    int32_t* arrived;  // [B][Hk][max_blocks]
+    int32_t* arrived;  // [B][Hk][max_blocks][COUNTERS]: the groups, if any, and the parts of each
     char* slots;       // [grid][2][SLOT]
 };
 
@@ -973,6 +979,7 @@ struct Worker {
                     for (int dq = 0; dq < C::DQ; ++dq) acc[rt][dq] = acc[rt][dq] * w0 + x[u][dq] * w1;
                 }
             }
+            m[rt] = top;
             l[rt] = sum;
         }
     }
@@ -1099,25 +1106,42 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                     auto slot = [&](int64_t c) {
                         return plan.slots + ((c * plan.side + member) * 2 + (c == c0 ? 1 : 0)) * (int64_t)C::SLOT;
                     };
-                    int32_t* arrived = plan.arrived + ((int64_t)b * a.Hk + w.h) * plan.max_blocks + block;
-                    const int parts = (int)(c1 - c0) + 1;
-                    // Where all others have arrived, this part stays in registers.
-                    if constexpr (C::KEEP) {
-                        if (tid == 0)
-                            s_last = __hip_atomic_load(arrived, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+                    int32_t* arrived =
+                        plan.arrived + (((int64_t)b * a.Hk + w.h) * plan.max_blocks + block) * C::COUNTERS;
+                    const int parts = (int)(c1 - c0) + 1, mine = (int)(cluster - c0);
+                    const int group = C::COUNTERS > 1 ? mine / C::GROUP : 0;
+                    const int groups = C::COUNTERS > 1 ? (parts + C::GROUP - 1) / C::GROUP : 1;
+                    // Whether this workgroup is the last of n to arrive; where all others have, its
+                    // own part stays in registers (KEEP).
+                    auto last = [&](int32_t* counter, int n, char* own) {
+                        if constexpr (C::KEEP) {
+                            if (tid == 0)
+                                s_last = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
+                            __syncthreads();
+                            if (s_last) return true;
+                        }
+                        w.save(own);
                         __syncthreads();
-                        out = s_last != 0;
-                    }
-                    if (!out) {
-                        w.save(slot(cluster));
+                        if (tid == 0) s_last = atomicAdd(counter, 1) == n - 1;
                         __syncthreads();
-                        if (tid == 0) s_last = atomicAdd(arrived, 1) == parts - 1;
-                        __syncthreads();
-                        out = s_last != 0;
-                    }
-                    if (out) {
-                        w.join_parts(parts, (int)(cluster - c0), [&](int i) { return slot(c0 + i); });
-                        if (tid == 0) *arrived = 0;
+                        return s_last != 0;
+                    };
+                    // A group's result takes the place of its first part, which has been read by then.
+                    int at_level = mine, first = group * C::GROUP, n = min(C::GROUP, parts - first), step = 1;
+                    int32_t* counter = arrived + (C::COUNTERS > 1 ? 1 + group : 0);
+#pragma unroll 1
+                    for (int level = 0;; ++level) {
+                        if (!last(counter, n, slot(c0 + at_level))) break;
+                        w.join_parts(n, (at_level - first) / step, [&](int i) { return slot(c0 + first + i * step); });
+                        if (tid == 0) *counter = 0;
+                        out = C::COUNTERS == 1 || level == 1 || groups == 1;
+                        if (out) break;
+                        at_level = first;
+                        first = 0;
+                        n = groups;
+                        step = C::GROUP;
+                        counter = arrived;
+                        __syncthreads();                 // s_last has been read
                     }
                 }
                 if (out) w.write(block, w.s.poison);
@@ -1143,7 +1167,7 @@ inline Plan make_plan(int B, int N, int group, int Hk, bool dense, char* ws) {
     p.side = dense ? (blocks + rounds - 1) / rounds : 1;
     p.clusters = p.grid / p.side;
     p.max_blocks = blocks;
-    const size_t counters = ((size_t)B * Hk * blocks * 4 + 255) / 256 * 256;
+    const size_t counters = ((size_t)B * Hk * blocks * C::COUNTERS * 4 + 255) / 256 * 256;
     p.arrived = (int32_t*)ws;
     p.slots = ws + counters;
     return p;
