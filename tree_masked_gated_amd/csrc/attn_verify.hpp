@@ -19,6 +19,18 @@
 // transposing 64-bit read (four keys of one column per lane); for fp32 its elements are
 // single words.
 //
+// Two ways through the keys, by the rows that share them:
+//   - up to 16 rows (next tokens, small trees): the four waves take 32 keys each, from memory to
+//     registers to LDS and without a barrier, the next tile's loads under way while one is
+//     computed.  Bound by reading the cache: 64 tokens over up to 32k keys, 2.1 GB, 400 us, 5.4 TB/s.
+//   - more rows: the waves share tiles that go from memory to LDS directly, two or three tiles
+//     deep.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences, 0.83 TFLOP: 890 us,
+//     929 TFLOP/s.  Matrix instructions fill 44 % of the cycles and vector instructions 54 %: a weight's
+//     scaling, exponential, conversion and sum cost as much as its products.  Every wave reads
+//     all of K and V from LDS (256 KB per tile of 64 keys, 2048 of the 4700 cycles that a tile takes).  With
+//     256 rows the two waves of a SIMD take turns at the two kinds of work (953 us; 1005 us in the
+//     same run's conditions where they do not).
+//
 // Work.  Tiles of all (sequence, key head, block of rows) form one line, cut into equal
 // shares, one per workgroup, so that contexts of very different lengths keep all CUs busy
 // to the end without the host knowing the lengths.  A block of rows whose keys were cut
@@ -1185,10 +1197,13 @@ inline hipError_t launch_cfg(const AttnArgs& a, hipStream_t stream) {
     return launch(attn_kernel<C>, dim3((unsigned)p.grid), dim3(C::NT), C::LDS, stream, a, p);
 }
 
-// The shape of the tiles by the rows that share keys, N group; f(Cfg) is called with the one
-// that applies.  Few rows: the waves split the keys and every key is read once, from memory
-// to registers to LDS, without a barrier.  Many rows: the waves split the rows and share
-// each tile.
+// The shape of the tiles by the rows that share keys, N group, and by the units (sequences times key
+// heads); f(Cfg) is called with the one that applies.  Few rows: the waves split the keys.  Many rows:
+// the waves split the rows and share each tile, the larger the block the fewer the reads of K and V.
+// Blocks are no larger than leaves half the CUs one each: then smaller ones join faster (one
+// sequence of four key heads, 256 rows each over 2800 keys: 131 us in blocks of 256, 40 us in blocks of
+// 64; 32 such sequences, 128 blocks: 93 us in blocks of 256, 98 us in blocks of 128).  17 to 32 rows take the tiles of
+// 64 (128 sequences, 32 rows over 2800 keys: 150 us; 165 us with the waves splitting the keys).
 template <int IO, int D, class F>
 inline auto choose(int rows, int units, F f) {
     if constexpr (IO == GDN_F32) {
