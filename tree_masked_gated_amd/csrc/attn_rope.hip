@@ -89,6 +89,13 @@ struct Piece<GDN_BF16> {
     }
 };
 
+// Rows leave past the L2: they are read by another launch, and kept there they push out the rows
+// still to be read (64 trees of 128 nodes, 36 heads of 128, 151 MB: 38 us, 25 us past it, 6.1 TB/s).
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void put16(char* p, uint4 v) {
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4*)p);
+}
+
 // Pieces of a head.  kHalf: a rotated piece is 16 bytes of the first coordinates and the
 // 16 bytes of their partners; kPairs: 16 bytes of adjacent pairs; the rest is copied, 16
 // bytes a piece.  kAny (rot does not divide into 16-byte pieces): one pair or one copied
@@ -202,7 +209,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
                 float f[E];
 #pragma unroll
                 for (int i = 0; i < E; ++i) f[i] = nan;
-                *(uint4*)(dst[u] + e * ES) = bad ? P::pack(f) : x[u];
+                put16(dst[u] + e * ES, bad ? P::pack(f) : x[u]);
             } else if constexpr (MODE == kHalf) {
                 float f[E], g[E], p[E], q[E];
                 P::unpack(x[u], f);
@@ -213,8 +220,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
                     p[i] = f[i] * cc - g[i] * ss;
                     q[i] = g[i] * cc + f[i] * ss;
                 }
-                *(uint4*)(dst[u] + c * E * ES) = P::pack(p);
-                *(uint4*)(dst[u] + (half + c * E) * ES) = P::pack(q);
+                put16(dst[u] + c * E * ES, P::pack(p));
+                put16(dst[u] + (half + c * E) * ES, P::pack(q));
             } else {
                 float f[E], p[E];
                 P::unpack(x[u], f);
@@ -224,7 +231,7 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
                     p[2 * i] = f[2 * i] * cc - f[2 * i + 1] * ss;
                     p[2 * i + 1] = f[2 * i + 1] * cc + f[2 * i] * ss;
                 }
-                *(uint4*)(dst[u] + c * E * ES) = P::pack(p);
+                put16(dst[u] + c * E * ES, P::pack(p));
             }
         }
     }

@@ -27,9 +27,9 @@
 //     deep.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences, 0.83 TFLOP: 890 us,
 //     929 TFLOP/s.  Matrix instructions fill 44 % of the cycles and vector instructions 54 %: a weight's
 //     scaling, exponential, conversion and sum cost as much as its products.  Every wave reads
-//     all of K and V from LDS (256 KB per tile of 64 keys, 2048 of the 4700 cycles that a tile takes).  With
-//     256 rows the two waves of a SIMD take turns at the two kinds of work (953 us; 1005 us in the
-//     same run's conditions where they do not).
+//     all of K and V from LDS (256 KB per tile of 64 keys, 1050 of the 4700 cycles that a tile takes).  With
+//     256 rows the two waves of a SIMD take turns at the two kinds of work (1005 us where they do
+//     not, 953 us where they do).
 //
 // Work.  Tiles of all (sequence, key head, block of rows) form one line, cut into equal
 // shares, one per workgroup, so that contexts of very different lengths keep all CUs busy
@@ -209,8 +209,10 @@ struct Worker {
     const int32_t* page_table;
     uint32_t top_page;                       // the largest page id met, as unsigned
     bool bad;
+    const bool once;                         // a key is read by one block of rows alone
 
-    __device__ __forceinline__ Worker(const AttnArgs& a_, char* lds_, int* flag) : a(a_), lds(lds_), s_flag(flag) {
+    __device__ __forceinline__ Worker(const AttnArgs& a_, char* lds_, int* flag, bool once_)
+        : a(a_), lds(lds_), s_flag(flag), once(once_) {
         const int tid = threadIdx.x;
         lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -271,6 +273,13 @@ struct Worker {
         return (uint64_t)id * (uint32_t)pool.page + (uint64_t)r * (uint32_t)pool.row;
     }
 
+    // Keys that one block of rows alone reads do not stay in the L2 (64 tokens over up to 32k keys:
+    // 394 us, 346 us past it, 6.2 TB/s).
+    static __device__ __forceinline__ uint4 get16_once(const char* p) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4*)p));
+    }
+
     // Loads a tile of the prefix into registers, through the page ids fetched before.
     __device__ __forceinline__ void load(int t) {
         const int j0 = key0(t) + tg / C::CPR;
@@ -280,8 +289,8 @@ struct Worker {
             const uint32_t r = j - quot(a.page, j) * a.page.d;
             top_page = max(top_page, (uint32_t)pid[i]);
             const uint32_t id = min((uint32_t)pid[i], (uint32_t)a.n_pages - 1u);
-            kreg[i] = *(const uint4*)(kbase + (offset16(a.kp, id, r) << 4));
-            vreg[i] = *(const uint4*)(vbase + (offset16(a.vp, id, r) << 4));
+            kreg[i] = get16_once(kbase + (offset16(a.kp, id, r) << 4));
+            vreg[i] = get16_once(vbase + (offset16(a.vp, id, r) << 4));
         }
     }
 
@@ -589,9 +598,16 @@ struct Worker {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             const char* from = base + (at[i] << 4);
-            if (piece_at(i) * E < a.d)       // LDS holds zeros where a row has ended
-                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-                             :: "s"(to + i * C::TG * 16), "v"(from) : "memory");
+            if (piece_at(i) * E < a.d) {     // LDS holds zeros where a row has ended
+                // bound by memory where the rows are few: 128 sequences, 64 rows over 2800 keys, 152 us,
+                // 135 us past the L2 (not with heads of 256: 454 us, 480 us)
+                if (C::WR < 8 && C::D <= 128 && once)
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
+                                 :: "s"(to + i * C::TG * 16), "v"(from) : "memory");
+                else
+                    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                                 :: "s"(to + i * C::TG * 16), "v"(from) : "memory");
+            }
         }
     }
     // All but the newest `later` pieces that each thread sent to LDS have arrived, for every wave.
@@ -1096,7 +1112,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
         start = s_pre[0];
     }
 
-    Worker<C> w(a, lds, s_flag);
+    Worker<C> w(a, lds, s_flag, plan.max_blocks == 1);
     while (at < end) {
         b = __builtin_amdgcn_readfirstlane(b);
         w.b = b;
