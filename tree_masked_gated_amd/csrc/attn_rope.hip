@@ -3,8 +3,9 @@
 // Pair t of a head's first `rot` coordinates is turned by a = position freq[t] and
 // scaled by amp; position = ctx[b] + depth[i].  Every head of a row shares the row's
 // angles, so a workgroup forms the cosines and sines of its rows once (in LDS) and
-// then streams all heads through them: the kernel is bound by the bytes of q and k,
-// read once and written once.
+// then streams all heads through them, the first pieces' loads under way meanwhile: the
+// kernel is bound by the bytes of q and k, read once and written once (64 trees of 128
+// nodes, 36 heads of 128, 151 MB: 23.2 us, 6.5 TB/s).
 //
 // Angles: position freq is formed in fp64 and reduced to [-pi/4, pi/4] by a two-part
 // pi/2 in fp64 (a position of 10^6 turns the fastest pair by 10^6 radians, of which
@@ -90,7 +91,7 @@ struct Piece<GDN_BF16> {
 };
 
 // Rows leave past the L2: they are read by another launch, and kept there they push out the rows
-// still to be read (64 trees of 128 nodes, 36 heads of 128, 151 MB: 38 us, 25 us past it, 6.1 TB/s).
+// still to be read (64 trees of 128 nodes, 36 heads of 128, 151 MB: 38 us; past it 24.6 us).
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void put16(char* p, uint4 v) {
     __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), (u32x4*)p);
@@ -112,6 +113,39 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const int64_t row0 = (int64_t)blockIdx.x * per_block;
     const int half = a.rot / 2;
+    const int H = a.Hq + a.Hk;
+    const int total = per_block * H * (int)pieces.d;
+    const char* src[kRopeUnroll];
+    char* dst[kRopeUnroll];
+    uint4 x[kRopeUnroll], y[kRopeUnroll];
+    int at[kRopeUnroll], rr[kRopeUnroll];
+    // Pieces it0, it0 + kRopeThreads, ... of the workgroup's rows: where they are, and their bytes.
+    auto fetch = [&](int it0) {
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            const int it = it0 + u * kRopeThreads;
+            const uint32_t hr = quot(pieces, it);
+            const uint32_t r = quot(heads, hr);
+            const int c = it - (int)(hr * pieces.d), h = (int)(hr - r * heads.d);
+            const int64_t gr = row0 + r;
+            rr[u] = it < total && gr < a.rows ? (int)r : -1;
+            if (rr[u] < 0) continue;
+            const bool isq = h < a.Hq;
+            const int hh = isq ? h : h - a.Hq;
+            const Rows& in = isq ? a.q : a.k;
+            const Rows& out = isq ? a.q_out : a.k_out;
+            src[u] = in.p + (gr * in.row + hh * in.head) * ES;
+            dst[u] = out.p + (gr * out.row + hh * out.head) * ES;
+            at[u] = c;
+            if constexpr (MODE != kAny) {
+                // element at which the piece begins
+                const int e = MODE == kHalf && c >= turned ? a.rot + (c - turned) * E : c * E;
+                x[u] = *(const uint4*)(src[u] + e * ES);
+                if (MODE == kHalf && c < turned) y[u] = *(const uint4*)(src[u] + (half + e) * ES);
+            }
+        }
+    };
+    fetch(tid);                              // under way while the angles are formed
     // Angles: wave w takes row w.
     const int64_t row = row0 + wave;
     if (wave < per_block) {
@@ -150,43 +184,10 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
         }
     }
     __syncthreads();
-    const int H = a.Hq + a.Hk;
-    const int total = per_block * H * (int)pieces.d;
-    for (int it0 = tid; it0 < total; it0 += kRopeThreads * kRopeUnroll) {
-        char* src[kRopeUnroll];
-        char* dst[kRopeUnroll];
-        uint4 x[kRopeUnroll], y[kRopeUnroll];
-        int at[kRopeUnroll], rr[kRopeUnroll];
+    for (int it0 = tid; it0 < total;) {
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            const int it = it0 + u * kRopeThreads;
-            rr[u] = -1;
-            if (it < total) {
-                const uint32_t hr = quot(pieces, it);
-                const uint32_t r = quot(heads, hr);
-                const int c = it - (int)(hr * pieces.d), h = (int)(hr - r * heads.d);
-                if (s_ok[r] != 0) {
-                    const int64_t gr = row0 + r;
-                    const bool isq = h < a.Hq;
-                    const int hh = isq ? h : h - a.Hq;
-                    const Rows& in = isq ? a.q : a.k;
-                    const Rows& out = isq ? a.q_out : a.k_out;
-                    src[u] = in.p + (gr * in.row + hh * in.head) * ES;
-                    dst[u] = out.p + (gr * out.row + hh * out.head) * ES;
-                    rr[u] = r;
-                    at[u] = c;
-                    if constexpr (MODE != kAny) {
-                        // element at which the piece begins
-                        const int e = MODE == kHalf && c >= turned ? a.rot + (c - turned) * E : c * E;
-                        x[u] = *(const uint4*)(src[u] + e * ES);
-                        if (MODE == kHalf && c < turned) y[u] = *(const uint4*)(src[u] + (half + e) * ES);
-                    }
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            if (rr[u] < 0) continue;
+            if (rr[u] < 0 || s_ok[rr[u]] == 0) continue;
             const float* cs = s_cos[rr[u]];
             const float* sn = s_sin[rr[u]];
             const int c = at[u];
@@ -234,6 +235,8 @@ __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs a, int per_
                 put16(dst[u] + c * E * ES, P::pack(p));
             }
         }
+        it0 += kRopeThreads * kRopeUnroll;
+        if (it0 < total) fetch(it0);
     }
 }
 
