@@ -22,10 +22,10 @@
 // Two ways through the keys, by the rows that share them:
 //   - up to 16 rows (next tokens, small trees): the four waves take 32 keys each, from memory to
 //     registers to LDS and without a barrier, the next tile's loads under way while one is
-//     computed.  Bound by reading the cache: 64 tokens over up to 32k keys, 2.1 GB, 400 us, 5.4 TB/s.
+//     computed.  Bound by reading the cache: 64 tokens over up to 32k keys, 2.1 GB, 346 us, 6.2 TB/s.
 //   - more rows: the waves share tiles that go from memory to LDS directly, two or three tiles
-//     deep.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences, 0.83 TFLOP: 890 us,
-//     929 TFLOP/s.  Matrix instructions fill 44 % of the cycles and vector instructions 54 %: a weight's
+//     deep.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences, 0.83 TFLOP: 865 us,
+//     956 TFLOP/s.  Matrix instructions fill 44 % of the cycles and vector instructions 54 %: a weight's
 //     scaling, exponential, conversion and sum cost as much as its products.  Every wave reads
 //     all of K and V from LDS (256 KB per tile of 64 keys, 1050 of the 4700 cycles that a tile takes).  With
 //     256 rows the two waves of a SIMD take turns at the two kinds of work (1005 us where they do
