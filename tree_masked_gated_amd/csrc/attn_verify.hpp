@@ -83,8 +83,9 @@ struct Cfg {
     // The last part of a block stays in registers where a thread's share of it is large (256 rows:
     // 131 KB that are neither written nor read); small ones take one way only.
     static constexpr bool KEEP = RT * DQ >= 16;
-    // Time that one more part takes to join, in tiles (measured with one sequence).
-    static constexpr float PART = IO == GDN_F32 || WR == 1 ? 0.05f : 1.0f;
+    // Time that one more part takes to join, in tiles (88 rows of two sequences over 660 keys: 41 us
+    // with 1, 36 us with 1/4; 384 rows over 206 keys 33 and 29; one sequence over 2800 keys 44 and 40).
+    static constexpr float PART = IO == GDN_F32 || WR == 1 ? 0.05f : 0.25f;
     // Parts that one workgroup joins.  A token's are small and many: groups of them are joined side by
     // side, then their results (one token over 4k and 32k keys: 23.5 and 46.5 us without groups, 19.8
     // and 40.0 with).  Parts of many rows are few, and a second step costs more than it saves there
