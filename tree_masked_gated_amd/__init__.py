@@ -116,15 +116,11 @@ def gdn_tree_cache_bytes(d: Dims) -> Dict[str, int]:
 
 # ------------------------------------------------------------ marshalling
 
-_torch_module = None
+_int32 = torch.int32
 
 
 def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
+    return torch
 
 
 def _io_dtype(d: Dims):
@@ -156,7 +152,6 @@ def _ptr(x, shape, dtype, name):
 def _stream(stream):
     if stream is None:
         # torch.cuda.current_stream().cuda_stream without its stream object (3 us of an 11 us call)
-        torch = _torch_module or _torch()
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
@@ -568,7 +563,7 @@ def _attn_rows(x, rows, heads, d, io, name):
 
 def _ints(x, shape, name):
     """Device pointer of a contiguous int32 tensor of this shape."""
-    if x.dtype is not _torch().int32 or not x.is_cuda or not x.is_contiguous() or x.shape != shape:
+    if x.dtype is not _int32 or not x.is_cuda or not x.is_contiguous() or x.shape != shape:
         raise ValueError(f"{name}: expected a contiguous int32 device tensor of shape {tuple(shape)}, "
                          f"got {x.dtype} {tuple(x.shape)}")
     return x.data_ptr()
