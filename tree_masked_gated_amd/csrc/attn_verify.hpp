@@ -40,6 +40,7 @@
 #pragma once
 
 #include "attn_common.hpp"
+#include "attn_schedule.hpp"
 
 namespace gdn {
 namespace attn {
@@ -578,7 +579,6 @@ struct Worker {
     __device__ __forceinline__ int piece_at(int i) const {
         return (tg % C::CPR) ^ swizzle<C>(tg / C::CPR + i * C::KSTEP);
     }
-    __device__ __forceinline__ Ahead locate(int t) { return locate(t, pid); }
     __device__ __forceinline__ Ahead locate(int t, const int (&ids)[NCH]) {
         const int j0 = key0(t) + tg / C::CPR;
         Ahead at;
@@ -611,11 +611,11 @@ struct Worker {
             }
         }
     }
-    // All but the newest `later` pieces that each thread sent to LDS have arrived, for every wave.
+    // All but the newest `later` pieces that this thread sent to LDS have arrived.  Loads that the
+    // compiler places among them only make the wait longer.
     template <int later>
-    static __device__ __forceinline__ void arrive() {
+    static __device__ __forceinline__ void wait() {
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(later) : "memory");
-        __syncthreads();
     }
     // A barrier between the halves of a tile.  This wave's reads of LDS have returned; what it has
     // under way to LDS is waited for elsewhere.
@@ -626,114 +626,94 @@ struct Worker {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
     }
-    // Tiles [t0, full).  While the values of tile t are added, the scores of t + 1 are formed: both
-    // products and the exponentials between them are independent and fill each other's gaps.
-    // Slot t % STAGES of LDS holds K of t until these scores, V of t until these values are done.
+    // Tiles [t0, full), in the order of attn_schedule.hpp.  While the values of tile t are added, the
+    // scores of t + 1 are formed: both products and the exponentials between them are independent
+    // and fill each other's gaps.
+    struct Walk {
+        Worker& w;
+        const char* const kb;                // row 0 of page 0
+        const char* const vb;
+        Ahead old, at;
+        int ids[NCH];
+        f32x4 sc[RT][KTILES];
+        Weights p[RT][PX];
+        bf16x8 f[kFrags];
+
+        __device__ __forceinline__ void fetch(int t) { w.fetch_pages(t); }
+        __device__ __forceinline__ void keep() {
+#pragma unroll
+            for (int i = 0; i < NCH; ++i) ids[i] = w.pid[i];
+        }
+        __device__ __forceinline__ void locate(int t) {
+            old = at;
+            at = w.locate(t, w.pid);
+        }
+        __device__ __forceinline__ void locate_kept(int t) {
+            old = at;
+            at = w.locate(t, ids);
+        }
+        __device__ __forceinline__ void send_k(int slot) { w.to_lds(kb, at.k, w.ktile(slot)); }
+        __device__ __forceinline__ void send_v(int slot) { w.to_lds(vb, old.v, w.vtile(slot)); }
+        // Sends of this thread, all but those of one tile's K (and V), have arrived.
+        __device__ __forceinline__ void wait_k() const {
+            if (w.a.d < C::D)
+                wait<0>();
+            else
+                wait<NCH>();
+        }
+        __device__ __forceinline__ void wait_sent(bool all) const {
+            if (all || w.a.d < C::D)
+                wait<0>();
+            else
+                wait<2 * NCH>();
+        }
+        __device__ __forceinline__ void barrier() const { __syncthreads(); }
+        __device__ __forceinline__ void turn() const { Worker::turn(); }
+        __device__ __forceinline__ void scores(int slot) { w.scores(w.ktile(slot), sc); }
+        __device__ __forceinline__ void early(int here, int next) {
+#pragma unroll
+            for (int u = 0; u < kEarly; ++u) f[u] = w.fragment(u, w.vtile(here), w.ktile(next));
+        }
+        __device__ __forceinline__ void weights() {
+            w.raise(sc);
+            w.weigh(sc, p);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int x = 0; x < PX; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
+        }
+        __device__ __forceinline__ void products(int here, int next) {
+            __builtin_amdgcn_s_setprio(1);
+            w.products(w.vtile(here), w.ktile(next), p, f, sc);
+            __builtin_amdgcn_s_setprio(0);
+        }
+        __device__ __forceinline__ void tile(int here, int next) {
+            w.raise(sc);
+            f32x4 sc1[RT][KTILES];
+            w.scores(w.ktile(next), sc1);
+            w.weigh(sc, p);
+            w.values(w.vtile(here), p);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int x = 0; x < KTILES; ++x) sc[rt][x] = sc1[rt][x];
+        }
+        __device__ __forceinline__ void finish(int here) {
+            w.raise(sc);
+            w.weigh(sc, p);
+            w.values(w.vtile(here), p);
+        }
+    };
     __device__ __forceinline__ void run_prefix(int t0, int full) {
-        constexpr int S = C::STAGES;
         if (a.d < C::D) {
             for (int i = threadIdx.x; i < C::LDS / 16; i += C::NT) ((uint4*)lds)[i] = uint4{0, 0, 0, 0};
             __syncthreads();
         }
-        const char* kb = a.kp.p + (int64_t)h * a.kp.head;
-        const char* vb = a.vp.p + (int64_t)h * a.vp.head;
-        const int last = full - 1;
-        fetch_pages(t0);
-        Ahead at = locate(t0);
-        to_lds(kb, at.k, ktile(0));
-#pragma unroll
-        for (int i = 1; i < S; ++i) {
-            fetch_pages(min(t0 + i, last));
-            to_lds(vb, at.v, vtile(i - 1));
-            at = locate(min(t0 + i, last));
-            to_lds(kb, at.k, ktile(i));
-        }
-        fetch_pages(min(t0 + S, last));
-        arrive<0>();
-        f32x4 sc[RT][KTILES];
-        scores(ktile(0), sc);
-        int here = 0, next = 1, prev = S - 1;    // slots of t, t + 1 and t - 1
-        if constexpr (C::WR == 8) {
-            // Two waves share a SIMD.  The second four run half a tile behind the first, so that one
-            // of the two has matrix work while the other forms weights; a barrier after each half
-            // keeps them so.  Per tile: weights(t) | values(t), scores(t + 1) |.  The slots that a
-            // wave's second half reads are filled when any wave's previous second half ends, and
-            // both groups are done with those of t - 1 when any wave's second half of t begins.
-            static_assert(S == 3, "slots");
-            Ahead old = at;
-            at = locate(min(t0 + S, last));
-            fetch_pages(min(t0 + S + 1, last));
-            if (wr >= 4) turn();
-            for (int t = t0; t < last; ++t) {
-                bf16x8 f[kFrags];
-#pragma unroll
-                for (int u = 0; u < kEarly; ++u) f[u] = fragment(u, vtile(here), ktile(next));
-                raise(sc);
-                Weights p[RT][PX];
-                weigh(sc, p);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int x = 0; x < PX; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
-                turn();
-                int ids[NCH];
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) ids[i] = pid[i];
-                fetch_pages(min(t + S + 2, last));
-                if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
-                if (t + S < full) to_lds(kb, at.k, ktile(here));
-                old = at;
-                at = locate(min(t + S + 1, last), ids);
-                __builtin_amdgcn_s_setprio(1);
-                products(vtile(here), ktile(next), p, f, sc);
-                __builtin_amdgcn_s_setprio(0);
-                if (t + S >= full || a.d < C::D)
-                    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                else
-                    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * NCH) : "memory");
-                turn();
-                prev = here;
-                here = next;
-                next = next + 1 == S ? 0 : next + 1;
-            }
-            if (wr < 4) turn();
-            raise(sc);
-            Weights p[RT][PX];
-            weigh(sc, p);
-            values(vtile(here), p);
-        } else {
-            for (int t = t0; t < last; ++t) {
-                // K of t + 1 and V of t are needed; K of t and V of t - 1 are done with.  Fewer pieces
-                // are under way near the end, and where rows have ended not every wave has some.
-                if (S == 2 || t + S > last || t == t0 || a.d < C::D)
-                    arrive<0>();
-                else
-                    arrive<(S - 2) * 2 * NCH>();
-                const Ahead old = at;
-                at = locate(min(t + S, last));
-                fetch_pages(min(t + S + 1, last));
-                if (t + S - 1 < full) to_lds(vb, old.v, vtile(prev));
-                if (t + S < full) to_lds(kb, at.k, ktile(here));
-                raise(sc);
-                f32x4 sc1[RT][KTILES];
-                Weights p[RT][PX];
-                scores(ktile(next), sc1);
-                weigh(sc, p);
-                values(vtile(here), p);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int x = 0; x < KTILES; ++x) sc[rt][x] = sc1[rt][x];
-                prev = here;
-                here = next;
-                next = next + 1 == S ? 0 : next + 1;
-            }
-            arrive<0>();
-            raise(sc);
-            Weights p[RT][PX];
-            weigh(sc, p);
-            values(vtile(here), p);
-        }
+        Walk o{*this, a.kp.p + (int64_t)h * a.kp.head, a.vp.p + (int64_t)h * a.vp.head};
+        if constexpr (C::WR == 8)
+            walk_in_turns<C::STAGES>(t0, full, wr < 4, o);   // the two waves of a SIMD
+        else
+            walk_in_step<C::STAGES>(t0, full, o);
     }
 
     // Adds the infinities and NaN of this part's values to the rows that see them (a cold path: one
