@@ -107,7 +107,8 @@ int gdn_attn_rope(const gdn_attn_dims* dims, const gdn_rope_dims* rope, const in
 
 /* Bytes of the workspace of gdn_attn_verify.  It is zeroed once, when it is
  * allocated; every call leaves it ready for the next.  One workspace serves
- * calls of these dims that follow each other on a stream, not concurrent ones. */
+ * calls that follow each other on a stream, not concurrent ones.  They may be of
+ * any dims that need no more bytes; fewer sequences or nodes never need more. */
 int gdn_attn_workspace_bytes(const gdn_attn_dims* dims, size_t* bytes);
 
 /*

@@ -605,7 +605,8 @@ def gdn_attn_workspace_bytes(d: AttnDims) -> int:
 
 
 def attn_workspace(d: AttnDims, device="cuda"):
-    """A zeroed workspace for gdn_attn_verify calls of these dims, one after the other."""
+    """A zeroed workspace for gdn_attn_verify calls, one after the other, of these dims or of any that need
+    no more bytes (fewer sequences, smaller trees)."""
     torch = _torch()
     return torch.zeros(max(gdn_attn_workspace_bytes(d), 16), dtype=torch.uint8, device=device)
 
@@ -621,7 +622,7 @@ def gdn_attn_verify(d: AttnDims, cache, table, ctx, q, k, v, anc_mask, tree_stat
         raise ValueError("table: expected [B, width]")
     if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() or \
             workspace.numel() < _workspace_bytes(d):
-        raise ValueError(f"workspace: expected {_workspace_bytes(d)} contiguous bytes (attn_workspace)")
+        raise ValueError(f"workspace: expected {_workspace_bytes(d)} contiguous bytes or more (attn_workspace)")
     _call("gdn_attn_verify", ctypes.byref(d), off, _cache_ref(cache), layer,
           _ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
           _attn_rows(q, T, d.h_q, d.d, io, "q"), _attn_rows(k, T, d.h_kv, d.d, io, "k"),

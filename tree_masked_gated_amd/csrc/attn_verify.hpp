@@ -36,7 +36,9 @@
 // to the end without the host knowing the lengths.  A block of rows whose keys were cut
 // leaves partial results (m, l, acc in fp32) in the workspace; the workgroup that arrives
 // last, by a counter, joins them in the order of the keys, so that results do not depend
-// on the order of arrival.
+// on the order of arrival.  Of the blocks that begin in a share at most the last one is cut, so
+// that a share's counters and slots serve batches of any sizes, and calls of different ones
+// may follow each other on one workspace.
 #pragma once
 
 #include "attn_common.hpp"
@@ -49,6 +51,7 @@ constexpr int kCUs = 256, kXcds = 8;
 constexpr int kMaxCtx = 0x7fff0000;          // key indexes, whole tiles of them, are 32 bits
 constexpr float kLag = 8.0f;
 constexpr int kMaxParts = 64;                // pieces of one block of rows
+constexpr int kCounterBytes = 18432;         // arrival counters, the workspace's first bytes: zero between calls
 constexpr float kLog2e = 1.4426950408889634f;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -93,6 +96,7 @@ struct Cfg {
     // (one tree of 128 rows over 4k keys: 39 us without, 43 with).
     static constexpr int GROUP = WR == 1 ? 8 : kMaxParts;
     static constexpr int COUNTERS = GROUP < kMaxParts ? 1 + kMaxParts / GROUP : 1;
+    static_assert(kCUs * OCC * COUNTERS * 4 <= kCounterBytes, "counters of all shares");
     static_assert(LDS + 4096 <= kMaxLds, "LDS of a workgroup");
     static_assert(TG % CPR == 0 && NCH >= 1, "a thread keeps its piece of the row");
     static_assert(KT % 32 == 0 && DT % WK == 0, "mask words, columns of the joining waves");
@@ -104,7 +108,8 @@ struct Plan {
     int side;          // C: workgroups that take neighbouring blocks of rows over the same keys
     int clusters;      // grid / C
     int max_blocks;    // blocks of rows of the largest tree
-    int32_t* arrived;  // [B][Hk][max_blocks][COUNTERS]: the groups, if any, and the parts of each
+    int32_t* arrived;  // [clusters][side][COUNTERS] of the block that is cut at the share's end: its groups,
+                       // if any, and the parts of each
     char* slots;       // [grid][2][SLOT]
 };
 
@@ -706,7 +711,7 @@ struct Worker {
     };
     __device__ __forceinline__ void run_prefix(int t0, int full) {
         if (a.d < C::D) {
-            for (int i = threadIdx.x; i < C::LDS / 16; i += C::NT) ((uint4*)lds)[i] = uint4{0, 0, 0, 0};
+            for (int i = wk * C::TG + tg; i < C::LDS / 16; i += C::NT) ((uint4*)lds)[i] = uint4{0, 0, 0, 0};
             __syncthreads();
         }
         Walk o{*this, a.kp.p + (int64_t)h * a.kp.head, a.vp.p + (int64_t)h * a.vp.head};
@@ -1109,15 +1114,14 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                 w.begin(block);
                 if (!w.s.poison) w.run((int)(at - us), (int)(stop - us));
                 w.join_waves();
-                const int64_t c0 = us / share, c1 = (ue - 1) / share;
+                const int c0 = (int)(us / share), c1 = (int)((ue - 1) / share);
                 bool out = c0 == c1;
                 if (!out) {
-                    auto slot = [&](int64_t c) {
+                    auto slot = [&](int c) {
                         return plan.slots + ((c * plan.side + member) * 2 + (c == c0 ? 1 : 0)) * (int64_t)C::SLOT;
                     };
-                    int32_t* arrived =
-                        plan.arrived + (((int64_t)b * a.Hk + w.h) * plan.max_blocks + block) * C::COUNTERS;
-                    const int parts = (int)(c1 - c0) + 1, mine = (int)(cluster - c0);
+                    int32_t* arrived = plan.arrived + (c0 * plan.side + member) * C::COUNTERS;
+                    const int parts = c1 - c0 + 1, mine = cluster - c0;
                     const int group = C::COUNTERS > 1 ? mine / C::GROUP : 0;
                     const int groups = C::COUNTERS > 1 ? (parts + C::GROUP - 1) / C::GROUP : 1;
                     // Whether this workgroup is the last of n to arrive; where all others have, its
@@ -1142,7 +1146,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
                     for (int level = 0;; ++level) {
                         if (!last(counter, n, slot(c0 + at_level))) break;
                         w.join_parts(n, (at_level - first) / step, [&](int i) { return slot(c0 + first + i * step); });
-                        if (tid == 0) *counter = 0;
+                        if (tid == 0) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
                         out = C::COUNTERS == 1 || level == 1 || groups == 1;
                         if (out) break;
                         at_level = first;
@@ -1165,7 +1169,7 @@ __global__ __launch_bounds__(C::NT, C::WAVES) void attn_kernel(AttnArgs a, Plan 
 // ------------------------------------------------------------------ host
 
 template <class C>
-inline Plan make_plan(int B, int N, int group, int Hk, bool dense, char* ws) {
+inline Plan make_plan(int N, int group, bool dense, char* ws) {
     Plan p;
     p.grid = kCUs * C::OCC;
     const int blocks = (N * group + C::BM - 1) / C::BM;
@@ -1176,21 +1180,19 @@ inline Plan make_plan(int B, int N, int group, int Hk, bool dense, char* ws) {
     p.side = dense ? (blocks + rounds - 1) / rounds : 1;
     p.clusters = p.grid / p.side;
     p.max_blocks = blocks;
-    const size_t counters = ((size_t)B * Hk * blocks * C::COUNTERS * 4 + 255) / 256 * 256;
     p.arrived = (int32_t*)ws;
-    p.slots = ws + counters;
+    p.slots = ws + kCounterBytes;
     return p;
 }
 
 template <class C>
-inline size_t plan_bytes(int B, int N, int group, int Hk) {
-    const Plan p = make_plan<C>(B, N, group, Hk, true, nullptr);
-    return (size_t)(p.slots - (char*)p.arrived) + (size_t)p.grid * 2 * C::SLOT;
+constexpr size_t plan_bytes() {
+    return kCounterBytes + (size_t)kCUs * C::OCC * 2 * C::SLOT;
 }
 
 template <class C>
 inline hipError_t launch_cfg(const AttnArgs& a, hipStream_t stream) {
-    const Plan p = make_plan<C>(a.B, a.N, a.group, a.Hk, a.offsets == nullptr, a.ws);
+    const Plan p = make_plan<C>(a.N, a.group, a.offsets == nullptr, a.ws);
     return launch(attn_kernel<C>, dim3((unsigned)p.grid), dim3(C::NT), C::LDS, stream, a, p);
 }
 
@@ -1229,7 +1231,7 @@ inline hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 }
 template <int IO, int D>
 inline size_t bytes_d(int B, int N, int group, int Hk) {
-    return choose<IO, D>(N * group, B * Hk, [&](auto c) { return plan_bytes<decltype(c)>(B, N, group, Hk); });
+    return choose<IO, D>(N * group, B * Hk, [](auto c) { return plan_bytes<decltype(c)>(); });
 }
 
 }  // namespace attn
