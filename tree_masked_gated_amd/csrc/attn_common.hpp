@@ -46,7 +46,7 @@ __device__ __forceinline__ uint32_t quot(FastDiv f, uint32_t n) {
 // Launch a kernel; the status is this launch's own (an earlier call's error stays where it is).
 template <class... P>
 inline hipError_t launch(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t stream, P... args) {
-    if (lds > 32 * 1024) {                   // with the static part, beyond the default limit
+    if (lds > 0) {                           // with the static part it may pass the default limit of 64 KiB
         hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
         if (e != hipSuccess) return e;
     }
