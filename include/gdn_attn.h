@@ -145,7 +145,7 @@ int gdn_attn_verify(const gdn_attn_dims* dims, const int32_t* offsets, const gdn
  *   path, path_len  as gdn_tree_commit (ragged: gdn_tree_commit_ragged) writes them
  *   new_len [B] int32  out: ctx + path_len; ctx where path_len <= 0; -1 where rows
  *                      have no place (ctx < 0, the table is too narrow or names no
- *                      page of the pool there) or path has an entry that is no node:
+ *                      page of the pool there, ctx + path_len > 2^31 - 1) or path has an entry that is no node:
  *                      then nothing of the sequence is appended.  Not ctx itself
  *                      (GDN_ERR_ALIAS): several workgroups read that.
  *

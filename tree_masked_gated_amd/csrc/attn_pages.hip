@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
     const int m = bad ? 0 : max(want, 0);
     if (m > 0) {
         const int64_t last = (len + m - 1) / (int64_t)a.page.d;
-        bad |= last >= a.width;
+        bad |= last >= a.width || len + m > 0x7fffffff;      // new_len has 31 bits
         if (!bad) {
             for (int t = tid; t < m; t += kThreads) {
                 const int i = a.path[rows.row0 + t];
