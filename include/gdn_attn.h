@@ -116,6 +116,7 @@ int gdn_attn_workspace_bytes(const gdn_attn_dims* dims, size_t* bytes);
  *
  *   cache     layer `layer` of the pools; they hold the prefixes alone
  *   table     [B][width] int32  page of rows page_rows c .. of sequence b, at [b][c]
+ *             (NULL where width is 0: no sequence has a prefix)
  *   ctx       [B] int32         rows of each prefix, 0 allowed
  *   q, k, v   [T] rows          of the tree's nodes (rotated already)
  *   anc_mask  [B][N][ceil(N/32)] int32, tree_status [B] int32: gdn_tree_cache's.

@@ -623,12 +623,14 @@ def gdn_attn_verify(d: AttnDims, cache, table, ctx, q, k, v, anc_mask, tree_stat
     if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() or \
             workspace.numel() < _workspace_bytes(d):
         raise ValueError(f"workspace: expected {_workspace_bytes(d)} contiguous bytes or more (attn_workspace)")
-    _call("gdn_attn_verify", ctypes.byref(d), off, _cache_ref(cache), layer,
-          _ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
-          _attn_rows(q, T, d.h_q, d.d, io, "q"), _attn_rows(k, T, d.h_kv, d.d, io, "k"),
-          _attn_rows(v, T, d.h_kv, d.d, io, "v"), _ints(anc_mask, (B, N, (N + 31) // 32), "anc_mask"),
-          _ints(tree_status, (B,), "tree_status"), _attn_rows(o, T, d.h_q, d.d, io, "o"),
-          workspace.data_ptr(), _stream(stream))
+    args = (_ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
+            _attn_rows(q, T, d.h_q, d.d, io, "q"), _attn_rows(k, T, d.h_kv, d.d, io, "k"),
+            _attn_rows(v, T, d.h_kv, d.d, io, "v"), _ints(anc_mask, (B, N, (N + 31) // 32), "anc_mask"),
+            _ints(tree_status, (B,), "tree_status"), _attn_rows(o, T, d.h_q, d.d, io, "o"))
+    if T == 0:                                   # trees without nodes: no row of o
+        return
+    _call("gdn_attn_verify", ctypes.byref(d), off, _cache_ref(cache), layer, *args, workspace.data_ptr(),
+          _stream(stream))
 
 
 @functools.lru_cache(maxsize=None)
@@ -648,10 +650,13 @@ def gdn_attn_commit(d: AttnDims, cache, table, ctx, k, v, path, path_len, new_le
     off, T = _attn_offsets(offsets, d, k)
     if table.dim() != 2:
         raise ValueError("table: expected [B, width]")
+    at = _ints(ctx, (B,), "ctx")
+    rows = [_attn_rows(k, T, d.h_kv, d.d, io, "k"), _attn_rows(v, T, d.h_kv, d.d, io, "v")]
+    nodes = _ints(path, (B, d.n_nodes) if offsets is None else (T,), "path")
+    if T == 0:                                   # trees without nodes: their tensors have no memory, and none is read
+        rows, nodes = [AttnRows(at, d.d, d.d)] * 2, at
     _call("gdn_attn_commit", ctypes.byref(d), off, _cache_ref(cache), layer,
-          _ints(table, (B, table.shape[1]), "table"), table.shape[1], _ints(ctx, (B,), "ctx"),
-          _attn_rows(k, T, d.h_kv, d.d, io, "k"), _attn_rows(v, T, d.h_kv, d.d, io, "v"),
-          _ints(path, (B, d.n_nodes) if offsets is None else (T,), "path"),
+          _ints(table, (B, table.shape[1]), "table"), table.shape[1], at, *rows, nodes,
           _ints(path_len, (B,), "path_len"), _ints(new_len, (B,), "new_len"), _stream(stream))
 
 

@@ -55,14 +55,16 @@ int check_cache(const gdn_paged_cache* c) {
                          c->io_dtype);
 }
 
-// The cache against the dims of a call on one of its layers.
-int check_layer(const gdn_attn_dims* d, const gdn_paged_cache* c, int32_t layer, int32_t width) {
+// The cache against the dims of a call on one of its layers; a table without columns is never read.
+int check_layer(const gdn_attn_dims* d, const gdn_paged_cache* c, int32_t layer, const int32_t* table,
+                int32_t width) {
     int rc = check_cache(c);
     if (rc) return rc;
     if (c->io_dtype != d->io_dtype) return GDN_ERR_DTYPE;
     if (c->h_kv != d->h_kv || c->d != d->d || layer < 0 || layer >= c->n_layers || width < 0 || width > (1 << 20))
         return GDN_ERR_DIMS;
-    return GDN_OK;
+    if (!table && width > 0) return GDN_ERR_NULL;
+    return misaligned(table) ? GDN_ERR_ALIGN : GDN_OK;
 }
 
 int check_offsets(const int32_t* offsets) { return misaligned(offsets, 4) ? GDN_ERR_ALIGN : GDN_OK; }
@@ -167,11 +169,11 @@ int gdn_attn_verify(const gdn_attn_dims* dims, const int32_t* offsets, const gdn
     if (rc) return rc;
     if (!(dims->scale > 0.0f) || !isfinite(dims->scale)) return GDN_ERR_DIMS;
     if (dims->batch == 0) return GDN_OK;
-    rc = check_layer(dims, cache, layer, width);
+    rc = check_layer(dims, cache, layer, table, width);
     if (rc) return rc;
     rc = check_rows({q, k, v, o}, dims->io_dtype);
     if (rc) return rc;
-    rc = check_ints({table, ctx, (const int32_t*)anc_mask, tree_status});
+    rc = check_ints({ctx, (const int32_t*)anc_mask, tree_status});
     if (rc) return rc;
     if (!workspace) return GDN_ERR_NULL;
     if (misaligned(workspace)) return GDN_ERR_ALIGN;
@@ -196,11 +198,11 @@ int gdn_attn_commit(const gdn_attn_dims* dims, const int32_t* offsets, const gdn
     int rc = check_dims(dims);
     if (rc) return rc;
     if (dims->batch == 0) return GDN_OK;
-    rc = check_layer(dims, cache, layer, width);
+    rc = check_layer(dims, cache, layer, table, width);
     if (rc) return rc;
     rc = check_rows({k, v}, dims->io_dtype);
     if (rc) return rc;
-    rc = check_ints({table, ctx, path, path_len, new_len});
+    rc = check_ints({ctx, path, path_len, new_len});
     if (rc) return rc;
     rc = check_offsets(offsets);
     if (rc) return rc;
