@@ -34,8 +34,9 @@
  *  - Pointers and all these strides are multiples of 16 bytes (GDN_ERR_ALIGN).
  *    Strides are not negative (GDN_ERR_DIMS).
  *
- * Sizes: 1 <= n_nodes <= 1024; h_kv >= 1; h_q a multiple of h_kv; n_nodes h_q / h_kv
- * <= 65536; d a multiple of 8, 8 <= d <= 256; io_dtype GDN_F32 or GDN_BF16.
+ * Sizes: 1 <= n_nodes <= 1024; 1 <= h_kv <= 8192; h_q a multiple of h_kv, <= 2^20; n_nodes
+ * h_q / h_kv <= 65536; d a multiple of 8, 8 <= d <= 256; io_dtype GDN_F32 or GDN_BF16;
+ * a page's keys of one layer at most 16 GiB.
  * batch = 0 launches nothing.
  *
  * Ragged batches are those of gdn_tree.h: `offsets` (device int32 [B + 1]) gives

@@ -12,11 +12,17 @@ using namespace gdn;
 
 bool misaligned(const void* p, uintptr_t to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
+// Heads up to which the kernels' 32-bit piece counts (a row's pieces, times four rows or times a
+// path of 1024) do not overflow, and 16-byte pieces of a page.
+constexpr int kMaxHeadsQ = 1 << 20, kMaxHeadsKv = 1 << 13;
+constexpr int64_t kMaxPagePieces = 1 << 30;
+
 int check_dims(const gdn_attn_dims* d) {
     if (!d) return GDN_ERR_NULL;
     if (d->io_dtype != GDN_F32 && d->io_dtype != GDN_BF16) return GDN_ERR_DTYPE;
     if (d->batch < 0 || d->n_nodes < 1 || d->n_nodes > kMaxNodes) return GDN_ERR_DIMS;
     if (d->h_kv < 1 || d->h_q < 1 || d->h_q % d->h_kv != 0) return GDN_ERR_DIMS;
+    if (d->h_q > kMaxHeadsQ || d->h_kv > kMaxHeadsKv) return GDN_ERR_DIMS;
     if (d->d < 8 || d->d > kMaxHead || d->d % 8 != 0) return GDN_ERR_DIMS;
     if ((int64_t)d->n_nodes * (d->h_q / d->h_kv) > 65536) return GDN_ERR_DIMS;
     return GDN_OK;
@@ -50,6 +56,7 @@ int check_cache(const gdn_paged_cache* c) {
     if (c->n_layers < 1 || c->n_pages < 1 || c->page_rows < 1 || c->page_rows > 65536 || c->h_kv < 1)
         return GDN_ERR_DIMS;
     if (c->d < 8 || c->d > kMaxHead || c->d % 8 != 0) return GDN_ERR_DIMS;
+    if ((int64_t)c->page_rows * c->h_kv > kMaxPagePieces / (c->d * elem(c->io_dtype) / 16)) return GDN_ERR_DIMS;
     if (misaligned(c->k) || misaligned(c->v)) return GDN_ERR_ALIGN;
     return check_strides({c->k_layer, c->k_page, c->k_row, c->k_head, c->v_layer, c->v_page, c->v_row, c->v_head},
                          c->io_dtype);
@@ -183,7 +190,7 @@ int gdn_attn_verify(const gdn_attn_dims* dims, const int32_t* offsets, const gdn
     auto rows_bytes = [es](const gdn_attn_rows* r) { return Rows{(char*)r->data, r->row * es, r->head * es}; };
     auto pool_bytes = [es](Pool p) { return Pool{p.p, p.page * es / 16, p.row * es / 16, p.head * es}; };
     for (int64_t x : {cache->k_page, cache->v_page, cache->k_row, cache->v_row})
-        if (x * es / 16 > 0xffffffffLL) return GDN_ERR_DIMS;
+        if (x / (16 / es) > 0xffffffffLL) return GDN_ERR_DIMS;
     AttnArgs a{dims->batch, dims->n_nodes, dims->h_q, dims->h_kv, group, dims->d, cache->n_pages, width,
                (dims->n_nodes + 31) / 32, dims->scale, fast_div(cache->page_rows), fast_div(group), offsets,
                pool_bytes(key_pool(cache, layer)), pool_bytes(value_pool(cache, layer)), rows_bytes(q), rows_bytes(k),
