@@ -127,8 +127,8 @@ int gdn_attn_workspace_bytes(const gdn_attn_dims* dims, size_t* bytes);
  *   o         [T][h_q][d] io    out
  *
  * Scores, running maximum, sum and output are fp32; with bf16 io the weights p
- * are rounded to bf16 for the product with v, and the sum is that of the rounded
- * weights.  Infinities and NaN in rows that a node does not see do not reach it.
+ * are rounded for the product with v, and the sum is that of the rounded weights: to 2^-16
+ * of each at most where up to 16 rows share a key head (n_nodes h_q / h_kv), to 2^-8 where more do.  Infinities and NaN in rows that a node does not see do not reach it.
  * The o rows of a sequence are NaN where tree_status is not 0, where ctx is outside
  * [0, min(page_rows width, 2^31 - 2^16)], or where an entry of the table that the prefix needs is not
  * a page of the pool; no page is read through such an entry.

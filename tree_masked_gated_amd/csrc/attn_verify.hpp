@@ -83,6 +83,12 @@ struct Cfg {
     static constexpr int DT = D / 16;                   // tiles of 16 columns
     static constexpr int DQ = DT / WK;                  // of these, a wave's share at the end
     static constexpr int KTILES = KT / 16;
+    // bf16 elements: a weight's product with V needs a bf16 operand.  Up to 16 rows, which are bound by
+    // reading the cache, it is the sum of two, the rounded weight and the rounded rest of it, 2^-16 from the
+    // weight at most (next tokens of 64 sequences over up to 32k keys: 348 us with one, 349 us with two).
+    // More rows are bound by the work on their weights and take one, 2^-8 from the weight at most (128-node
+    // trees of 64 sequences: 915 us with one, 1218 us with two; 88 rows of one sequence 105 and 128 us).
+    static constexpr int TERMS = IO == GDN_BF16 && WR == 1 ? 2 : 1;
     static constexpr int SLOT = BM * (D + 2) * 4;       // bytes of a partial result
     // The last part of a block stays in registers where a thread's share of it is large (256 rows:
     // 131 KB that are neither written nor read); small ones take one way only.
@@ -424,8 +430,8 @@ struct Worker {
 
     // Weights of a tile's keys from their scores, and their sum.
     typedef typename std::conditional<C::IO == GDN_F32, f32x4, bf16x8>::type Weights;
-    static constexpr int PX = C::IO == GDN_F32 ? KTILES : KTILES / 2;
-    __device__ __forceinline__ void weigh(f32x4 (&sc)[RT][KTILES], Weights (&p)[RT][PX]) {
+    static constexpr int PX = C::IO == GDN_F32 ? KTILES : KTILES / 2, NP = PX * C::TERMS;
+    __device__ __forceinline__ void weigh(f32x4 (&sc)[RT][KTILES], Weights (&p)[RT][NP]) {
         const float scale = a.scale * kLog2e;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -441,9 +447,8 @@ struct Worker {
                     l[rt] += (sc[rt][x][0] + sc[rt][x][1]) + (sc[rt][x][2] + sc[rt][x][3]);
                 }
             } else {
-                // The weights are rounded to bf16, 2^-8 of each at most: the product needs two bf16
-                // operands.  l sums the rounded ones, so that the weights' quotients add up to one
-                // and a row that sees one key gets that key's value exactly.
+                // l sums the terms that the product takes, so that the weights' quotients add up to
+                // one and a row that sees one key gets that key's value exactly.
                 const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
 #pragma unroll
                 for (int x = 0; x < KTILES / 2; ++x) {
@@ -456,6 +461,14 @@ struct Worker {
                         l[rt] = __builtin_amdgcn_fdot2_f32_bf16(v, one, l[rt], false);
                         p[rt][x][i] = v[0];
                         p[rt][x][i + 1] = v[1];
+                        if constexpr (C::TERMS == 2) {
+                            bf16x2 rest;
+                            rest[0] = (__bf16)(src[i & 3] - (float)v[0]);
+                            rest[1] = (__bf16)(src[(i & 3) + 1] - (float)v[1]);
+                            l[rt] = __builtin_amdgcn_fdot2_f32_bf16(rest, one, l[rt], false);
+                            p[rt][PX + x][i] = rest[0];
+                            p[rt][PX + x][i + 1] = rest[1];
+                        }
                     }
                 }
             }
@@ -463,7 +476,7 @@ struct Worker {
     }
 
     // acc += weights times a tile's values.
-    __device__ __forceinline__ void values(const char* vt, const Weights (&p)[RT][PX]) {
+    __device__ __forceinline__ void values(const char* vt, const Weights (&p)[RT][NP]) {
         const int g = lane >> 4, c16 = lane & 15;
         if constexpr (C::IO == GDN_F32) {
 #pragma unroll
@@ -499,7 +512,9 @@ struct Worker {
                     v = __builtin_shufflevector(vl, vh, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt)
-                        acc[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][x], acc[rt][dt], 0, 0, 0);
+#pragma unroll
+                        for (int y = x; y < NP; y += PX)
+                            acc[rt][dt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, p[rt][y], acc[rt][dt], 0, 0, 0);
                 }
             }
         }
@@ -524,7 +539,7 @@ struct Worker {
         const int x = (u - kPv) % KTILES, ks = (u - kPv) / KTILES;
         return *(const bf16x8*)(kt + (x * 16 + c16) * C::ROWB + ((ks * 4 + g) ^ swizzle<C>(c16)) * 16);
     }
-    __device__ __forceinline__ void products(const char* vt, const char* kt, const Weights (&p)[RT][PX],
+    __device__ __forceinline__ void products(const char* vt, const char* kt, const Weights (&p)[RT][NP],
                                              bf16x8 (&f)[kFrags], f32x4 (&sc)[RT][KTILES]) {
 #pragma unroll
         for (int u = 0; u < kFrags; ++u) {
@@ -566,7 +581,7 @@ struct Worker {
             }
         }
         raise(sc);
-        Weights p[RT][PX];
+        Weights p[RT][NP];
         weigh(sc, p);
         values(vtile(stage), p);
         if constexpr (MIXED) {
@@ -641,7 +656,7 @@ struct Worker {
         Ahead old, at;
         int ids[NCH];
         f32x4 sc[RT][KTILES];
-        Weights p[RT][PX];
+        Weights p[RT][NP];
         bf16x8 f[kFrags];
 
         __device__ __forceinline__ void fetch(int t) { w.fetch_pages(t); }
@@ -685,7 +700,7 @@ struct Worker {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-                for (int x = 0; x < PX; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
+                for (int x = 0; x < NP; ++x) asm volatile("" : "+v"(p[rt][x]));   // formed by here
         }
         __device__ __forceinline__ void products(int here, int next) {
             __builtin_amdgcn_s_setprio(1);
