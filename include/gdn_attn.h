@@ -214,8 +214,9 @@ int gdn_pages_free(const gdn_page_dims* dims, const int32_t* drop, int32_t* ref,
                    int32_t* held, int32_t* length, hipStream_t stream);
 
 /*
- * Move the held pages to the front of the pool: with m pages held, the i-th held page
- * at or past m goes to the i-th free page below m.  At most n pages are moved.
+ * Move the held pages, those with ref > 0, to the front of the pool: with m pages held, the
+ * i-th held page at or past m goes to the i-th free page below m.  At most n pages are
+ * moved.  `held` is not read.
  *   src, dst [n] int32, count [1] int32 out: the copies (gdn_pages_copy)
  *   remap [n_pages] int32 out: where each page's rows are afterwards
  * ref and table are brought in line; table entries that name no page stay.

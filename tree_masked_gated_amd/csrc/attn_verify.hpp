@@ -22,14 +22,17 @@
 // Two ways through the keys, by the rows that share them:
 //   - up to 16 rows (next tokens, small trees): the four waves take 32 keys each, from memory to
 //     registers to LDS and without a barrier, the next tile's loads under way while one is
-//     computed.  Bound by reading the cache: 64 tokens over up to 32k keys, 2.1 GB, 346 us, 6.2 TB/s.
-//   - more rows: the waves share tiles that go from memory to LDS directly, two or three tiles
-//     deep.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences, 0.83 TFLOP: 865 us,
-//     956 TFLOP/s.  Matrix instructions fill 44 % of the cycles and vector instructions 54 %: a weight's
-//     scaling, exponential, conversion and sum cost as much as its products.  Every wave reads
-//     all of K and V from LDS (256 KB per tile of 64 keys, 1050 of the 4700 cycles that a tile takes).  With
-//     256 rows the two waves of a SIMD take turns at the two kinds of work (1005 us where they do
-//     not, 953 us where they do).
+//     computed.  Bound by reading the cache: 64 tokens over up to 32k keys, 2.1 GB, 348 to 388 us on
+//     different cards, 5.6 to 6.2 TB/s.
+//   - more rows: the waves share two or three tiles that go from memory to LDS directly.  They are sent
+//     one or two tiles ahead, but not under way for that long: the compiler's waits for page ids count
+//     all loads, and take the pieces sent before with them, so that a piece has half a tile's time (256
+//     rows) or a tile's to arrive.  128 nodes x 8 query heads per key head over 4k-8k keys, 64 sequences,
+//     0.83 TFLOP: 890 us, 929 TFLOP/s.  Matrix instructions fill 44 % of the cycles, vector instructions
+//     55 %, and waves wait 32 % of theirs: a weight's scaling, exponential, conversion and sum cost as much
+//     as its products.  Every wave reads all of K and V from LDS (256 KB per tile of 64 keys, 1050 of the
+//     4700 cycles that a tile takes).  With 256 rows the two waves of a SIMD take turns at the two kinds of
+//     work (1005 us where they do not, 953 us where they do, when this was built).
 //
 // Work.  Tiles of all (sequence, key head, block of rows) form one line, cut into equal
 // shares, one per workgroup, so that contexts of very different lengths keep all CUs busy
@@ -87,7 +90,8 @@ struct Cfg {
     // reading the cache, it is the sum of two, the rounded weight and the rounded rest of it, 2^-16 from the
     // weight at most (next tokens of 64 sequences over up to 32k keys: 348 us with one, 349 us with two).
     // More rows are bound by the work on their weights and take one, 2^-8 from the weight at most (128-node
-    // trees of 64 sequences: 915 us with one, 1218 us with two; 88 rows of one sequence 105 and 128 us).
+    // trees of 64 sequences: 915 us with one, 1218 us with two; 128 rows of 64 sequences over 2800 keys 105
+    // and 128 us, 64 rows of 128 sequences 134 and 141 us).
     static constexpr int TERMS = IO == GDN_BF16 && WR == 1 ? 2 : 1;
     static constexpr int SLOT = BM * (D + 2) * 4;       // bytes of a partial result
     // The last part of a block stays in registers where a thread's share of it is large (256 rows:
@@ -95,6 +99,9 @@ struct Cfg {
     static constexpr bool KEEP = RT * DQ >= 16;
     // Time that one more part takes to join, in tiles (88 rows of two sequences over 660 keys: 41 us
     // with 1, 36 us with 1/4; 384 rows over 206 keys 33 and 29; one sequence over 2800 keys 44 and 40).
+    // All of these are blocks of 64 rows; blocks of 128 and 256 take the same value untuned.  For those of
+    // 256 it is too low: 32 sequences of four such blocks take 19 us without a prefix, 33 us over 64
+    // keys and 44 us over 128, which are one and two tiles more for a block.
     static constexpr float PART = IO == GDN_F32 || WR == 1 ? 0.05f : 0.25f;
     // Parts that one workgroup joins.  A token's are small and many: groups of them are joined side by
     // side, then their results (one token over 4k and 32k keys: 23.5 and 46.5 us without groups, 19.8
@@ -222,7 +229,7 @@ struct Worker {
     const int32_t* page_table;
     uint32_t top_page;                       // the largest page id met, as unsigned
     bool bad;
-    const bool once;                         // a key is read by one block of rows alone
+    const bool once;                         // a sequence's keys are read by one block of rows alone
 
     __device__ __forceinline__ Worker(const AttnArgs& a_, char* lds_, int* flag, bool once_)
         : a(a_), lds(lds_), s_flag(flag), once(once_) {
@@ -286,8 +293,10 @@ struct Worker {
         return (uint64_t)id * (uint32_t)pool.page + (uint64_t)r * (uint32_t)pool.row;
     }
 
-    // Keys that one block of rows alone reads do not stay in the L2 (64 tokens over up to 32k keys:
-    // 394 us, 346 us past it, 6.2 TB/s).
+    // Keys that one block of rows of the sequence reads do not stay in the L2 (64 tokens over 8k keys
+    // each: 218 us, 198 us past it).  Sequences that share pages read them again, and would find them
+    // there; the host does not know of them (the same where fours share their pages: 170 us, 183 us
+    // past it; 32 rows over 4k keys 99 and 122 us).
     static __device__ __forceinline__ uint4 get16_once(const char* p) {
         typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
         return __builtin_bit_cast(uint4, __builtin_nontemporal_load((const u32x4*)p));
@@ -591,8 +600,7 @@ struct Worker {
 
     // Waves that share tiles: the pieces of a tile go from the pools to LDS without passing
     // through registers.  A wave's 64 pieces land side by side, so that thread tg fills the place
-    // tg + i TG of the tile and fetches the piece that belongs there.  Keys are loaded two tiles
-    // ahead of the one whose values are being added, values one.
+    // tg + i TG of the tile and fetches the piece that belongs there.
     struct Ahead {
         uint64_t k[NCH], v[NCH];             // offsets in pieces of 16 bytes from the pools' data
     };
