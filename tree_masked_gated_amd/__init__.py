@@ -1,7 +1,7 @@
 """Python binding of libgdntree.so: rollback-free GDN draft-tree verification on
 MI355X (gfx950).
 
-The names mirror the C ABI in include/gdn_tree.h and include/gdn_attn.h.  This module only marshals
+The names mirror the C ABI in include/gdn_tree.h, gdn_attn.h and gdn_rule.h.  This module only marshals
 arguments: it checks that each torch tensor has the shape, dtype and
 contiguity the C ABI documents (so a kernel never reads past a buffer) and
 passes device pointers and the current HIP stream.  Every step of the
@@ -26,6 +26,8 @@ __all__ = [
     "PagedCache", "attn_dims", "rope_dims", "page_dims", "attn_workspace", "gdn_attn_workspace_bytes",
     "gdn_attn_rope", "gdn_attn_verify", "gdn_attn_commit", "gdn_pages_fork", "gdn_pages_reserve",
     "gdn_pages_copy", "gdn_pages_free", "gdn_pages_compact",
+    "RuleDims", "rule_dims", "rule_workspace", "gdn_rule_workspace_bytes", "gdn_rule_forward",
+    "gdn_rule_backward", "gdn_rule_step",
 ]
 
 GDN_F32, GDN_BF16 = 0, 1
@@ -708,3 +710,86 @@ def gdn_pages_compact(pd: PageDims, ref, table, held, src, dst, count, remap, st
           _ints(table, (pd.n_slots, pd.width), "table"), _ints(held, (pd.n_slots,), "held"),
           _ints(src, (n,), "src"), _ints(dst, (n,), "dst"), _ints(count, (1,), "count"),
           _ints(remap, (pd.n_pages,), "remap"), _stream(stream))
+
+
+# ---------------------------------------------------------------- the rule over whole sequences
+# Prompts, training sequences and single tokens through a Gated DeltaNet layer (include/gdn_rule.h).
+# Row tensors ([rows, heads, d]) may be strided slices; sequence b owns rows offsets[b] .. offsets[b+1] - 1.
+
+
+class RuleDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "h_k", "h_v", "d_k", "d_v", "io_dtype")]
+
+
+_rd = ctypes.POINTER(RuleDims)
+for _name, _args in {
+        "gdn_rule_workspace_bytes": [_rd, _i64, _i32, _sz],
+        "gdn_rule_forward": [_rd, _vp, _i64, _vp, _ar, _ar, _ar, _vp, _vp, _ar, _vp, _vp, _vp],
+        "gdn_rule_backward": [_rd, _vp, _i64, _vp, _ar, _ar, _ar, _vp, _vp, _ar, _vp, _ar, _ar, _ar] + [_vp] * 5,
+        "gdn_rule_step": [_rd, _vp, _i32, _ar, _ar, _ar, _vp, _vp, _vp, _ar, _vp]}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _i
+
+
+def rule_dims(batch, h_k, h_v, d_k, d_v, io_dtype) -> RuleDims:
+    if isinstance(io_dtype, str):
+        io_dtype = {"f32": GDN_F32, "bf16": GDN_BF16}[io_dtype]
+    return RuleDims(batch, h_k, h_v, d_k, d_v, io_dtype)
+
+
+def gdn_rule_workspace_bytes(d: RuleDims, n_rows, backward=False) -> int:
+    out = ctypes.c_size_t()
+    _call("gdn_rule_workspace_bytes", ctypes.byref(d), n_rows, int(backward), ctypes.byref(out))
+    return out.value
+
+
+def rule_workspace(d: RuleDims, n_rows, backward=False, device="cuda"):
+    """A workspace for gdn_rule_forward (or, with backward, gdn_rule_backward) of these dims and up to n_rows
+    rows.  Nothing of it lasts from call to call."""
+    return torch.empty(max(gdn_rule_workspace_bytes(d, n_rows, backward), 16), dtype=torch.uint8, device=device)
+
+
+def _rule_workspace(ws, d, T, backward):
+    need = gdn_rule_workspace_bytes(d, T, backward)
+    if ws.dtype != torch.uint8 or not ws.is_cuda or not ws.is_contiguous() or ws.numel() < need:
+        raise ValueError(f"workspace: expected {need} contiguous bytes or more (rule_workspace)")
+    return ws.data_ptr()
+
+
+def gdn_rule_forward(d: RuleDims, offsets, q, k, v, beta, g, o, workspace, S0=None, S_out=None, stream=None) -> None:
+    """Enqueue the rule along every sequence (see gdn_rule.h): o, and the states after the sequences."""
+    T, io, state = q.shape[0], _io_dtype(d), (d.batch, d.h_v, d.d_v, d.d_k)
+    _call("gdn_rule_forward", ctypes.byref(d), _ints(offsets, (d.batch + 1,), "offsets"), T,
+          _ptr(S0, state, torch.float32, "S0"), _attn_rows(q, T, d.h_k, d.d_k, io, "q"),
+          _attn_rows(k, T, d.h_k, d.d_k, io, "k"), _attn_rows(v, T, d.h_v, d.d_v, io, "v"),
+          _ptr(beta, (T, d.h_v), torch.float32, "beta"), _ptr(g, (T, d.h_v), torch.float32, "g"),
+          _attn_rows(o, T, d.h_v, d.d_v, io, "o"), _ptr(S_out, state, torch.float32, "S_out"),
+          _rule_workspace(workspace, d, T, False), _stream(stream))
+
+
+def gdn_rule_backward(d: RuleDims, offsets, q, k, v, beta, g, d_o, dq, dk, dv, dbeta, dlog_g, workspace, S0=None,
+                      dS_out=None, dS0=None, stream=None) -> None:
+    """Enqueue the gradients of gdn_rule_forward (see gdn_rule.h), from its inputs alone.  dlog_g is the
+    gradient with regard to ln g."""
+    T, io, state = q.shape[0], _io_dtype(d), (d.batch, d.h_v, d.d_v, d.d_k)
+    keys = lambda x, name: _attn_rows(x, T, d.h_k, d.d_k, io, name)  # noqa: E731
+    vals = lambda x, name: _attn_rows(x, T, d.h_v, d.d_v, io, name)  # noqa: E731
+    gate = lambda x, name: _ptr(x, (T, d.h_v), torch.float32, name)  # noqa: E731
+    _call("gdn_rule_backward", ctypes.byref(d), _ints(offsets, (d.batch + 1,), "offsets"), T,
+          _ptr(S0, state, torch.float32, "S0"), keys(q, "q"), keys(k, "k"), vals(v, "v"), gate(beta, "beta"),
+          gate(g, "g"), vals(d_o, "d_o"), _ptr(dS_out, state, torch.float32, "dS_out"), keys(dq, "dq"),
+          keys(dk, "dk"), vals(dv, "dv"), gate(dbeta, "dbeta"), gate(dlog_g, "dlog_g"),
+          _ptr(dS0, state, torch.float32, "dS0"), _rule_workspace(workspace, d, T, True), _stream(stream))
+
+
+def gdn_rule_step(d: RuleDims, q, k, v, beta, g, state, o, slot=None, stream=None) -> None:
+    """Enqueue one token of every sequence on a pool of states [slots, h_v, d_v, d_k], in place (see
+    gdn_rule.h).  slot: each sequence's place in the pool (-1: none), or None for its own number."""
+    B, io = d.batch, _io_dtype(d)
+    gate = lambda x, name: _ptr(x, (B, d.h_v), torch.float32, name)  # noqa: E731
+    n = state.shape[0]
+    _call("gdn_rule_step", ctypes.byref(d), None if slot is None else _ints(slot, (B,), "slot"), n,
+          _attn_rows(q, B, d.h_k, d.d_k, io, "q"), _attn_rows(k, B, d.h_k, d.d_k, io, "k"),
+          _attn_rows(v, B, d.h_v, d.d_v, io, "v"), gate(beta, "beta"), gate(g, "g"),
+          _ptr(state, (n, d.h_v, d.d_v, d.d_k), torch.float32, "state"), _attn_rows(o, B, d.h_v, d.d_v, io, "o"),
+          _stream(stream))

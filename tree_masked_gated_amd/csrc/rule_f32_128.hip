@@ -1,0 +1,7 @@
+// rule_f32_128.hip -- the chunked gated delta rule for f32 rows, d_k <= 128.
+#include "rule_kernels.hpp"
+
+namespace gdn {
+template hipError_t rule_forward_launch<GDN_F32, 128>(const RuleArgs&, hipStream_t);
+template hipError_t rule_backward_launch<GDN_F32, 128>(const RuleArgs&, hipStream_t);
+}  // namespace gdn

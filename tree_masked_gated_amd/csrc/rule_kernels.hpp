@@ -1,0 +1,1029 @@
+// rule_kernels.hpp -- the chunked gated delta rule on MFMA (see rule_common.hpp for the
+// mathematics), compiled for one element type and padded d_k per source file.
+#pragma once
+
+#include "rule_common.hpp"
+
+namespace gdn {
+
+// Rows of the LDS tiles are padded by 8 elements: 16-byte reads of 16 rows then spread over all banks.
+constexpr int kTp = kC + 8;
+
+// ------------------------------------------------------------------ prepare
+//
+// One workgroup of four waves per (chunk slot, key head).  Wave w owns row tile w (16 rows).
+// The chunk's keys and queries are laid out as matrix operands once, for every value head and
+// slice that reads them; the products K K^T and Q K^T are formed once per key head, and each of
+// its value heads makes its M and Y of them.  M is formed in fp32 (diagonal blocks by
+// substitution, the others by fp32 matrix instructions) and kept as bf16 terms.
+template <int IO, int DK, bool BACK>
+__global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
+    constexpr int P = kPlanes<IO>, R = kRound<IO>, KS = DK / 32, NT = DK / 16, LD = DK + 8;
+    constexpr int TP = kC + 4;                       // fp32 row, whole 16-byte pieces
+    __shared__ __attribute__((aligned(16))) uint16_t rows[P][kC][LD];
+    __shared__ __attribute__((aligned(16))) float xs[kC][TP];
+    __shared__ __attribute__((aligned(16))) float ts[kC][TP];
+    __shared__ double gam[kC];
+    __shared__ float bet[kC];
+
+    const int slot = blockIdx.x, hk = blockIdx.y;
+    const RuleChunk ch = rule_chunk(a, slot);
+    if (ch.n == 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const int row = 16 * wv + n;                     // this lane's row of an operand tile
+    const bool live = row < ch.n;
+    const int64_t grow = ch.row0 + (live ? row : 0);
+    const size_t key = (size_t)slot * a.Hk + hk;
+    constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
+
+    // K: operand fragments of its rows, and the rows in LDS
+    Planes<IO> kfr[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        kfr[s] = load_row8<IO>(a.k.p, grow * a.k.row + (int64_t)hk * a.k.head, 32 * s + 8 * q4, a.dk, a.vk, live);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            store_frag(a.kf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, kfr[s].p[p]);
+            *reinterpret_cast<bf16x8*>(&rows[p][row][32 * s + 8 * q4]) = kfr[s].p[p];
+        }
+    }
+    Planes<IO> qfr[KS];
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+        qfr[s] = load_row8<IO>(a.q.p, grow * a.q.row + (int64_t)hk * a.q.head, 32 * s + 8 * q4, a.dk, a.vq, live);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+            store_frag(a.qf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, qfr[s].p[p]);
+    }
+    __syncthreads();
+    // the lower row tiles of K K^T and Q K^T
+    f32x4 kk[4], qk[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        kk[j] = qk[j] = f32x4{0, 0, 0, 0};
+        if (j > wv) continue;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            bf16x8 b[P];
+            get8<P>(&rows[0][16 * j + n][32 * s + 8 * q4], kC * LD, b);
+            kk[j] = mma<P, P>(kfr[s].p, b, kk[j]);
+            qk[j] = mma<P, P>(qfr[s].p, b, qk[j]);
+        }
+    }
+    // transposed operands: 8 rows of one column per lane
+    auto transposed = [&](char* to) {
+        for (int t = wv; t < NT; t += 4)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    bf16x8 x;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = __builtin_bit_cast(__bf16, rows[p][32 * s + 8 * q4 + j][16 * t + n]);
+                    store_frag(to + key * kTile + ((p * NT + t) * 2 + s) * kFrag, lane, x);
+                }
+    };
+    transposed(a.kt);
+    if constexpr (BACK) {
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<bf16x8*>(&rows[p][row][32 * s + 8 * q4]) = qfr[s].p[p];
+        __syncthreads();
+        transposed(a.qt);
+    }
+
+    // fragments of a lower triangular tile, and of its transpose
+    auto keep = [&](const float (&v)[8], char* to, int f, auto planes) {
+        bf16x8 x[decltype(planes)::value];
+        split8(v, x);
+#pragma unroll
+        for (int p = 0; p < decltype(planes)::value; ++p) store_frag(to + (p * kTriFrags + f) * kFrag, lane, x[p]);
+    };
+    auto low = [&](const float (*x)[TP], char* to, auto planes) {
+        for (int f = wv; f < kTriFrags; f += 4) {
+            const int i = f < 2 ? f : 2 + (f - 2) / 2, s = f < 2 ? 0 : (f - 2) % 2;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = x[16 * i + n][32 * s + 8 * q4 + j];
+            keep(v, to, f, planes);
+        }
+    };
+    auto up = [&](const float (*x)[TP], char* to) {
+        for (int f = wv; f < kTriFrags; f += 4) {
+            const int i = f < 4 ? f / 2 : f - 2, s = f < 4 ? f % 2 : 1;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = x[32 * s + 8 * q4 + j][16 * i + n];
+            keep(v, to, f, std::integral_constant<int, kSum>());
+        }
+    };
+
+    for (int gi = 0; gi < a.group; ++gi) {
+        const int hv = hk * a.group + gi;
+        const size_t val = (size_t)slot * a.Hv + hv;
+        if (wv == 0) {                               // running sums of log2 g, in fp64
+            const bool in = lane < ch.n;
+            const int64_t at = (ch.row0 + (in ? lane : 0)) * a.Hv + hv;
+            const float b = in ? a.beta[at] : 0.f;
+            double x = in ? (double)log2f(a.g[at]) : 0.0;
+#pragma unroll
+            for (int off = 1; off < 64; off *= 2) {
+                const double y = __shfl_up(x, off);
+                if (lane >= off) x += y;
+            }
+            gam[lane] = x;
+            bet[lane] = b;
+            float* c = a.coef + val * 3 * kC;
+            c[lane] = exp2f((float)x);
+            c[kC + lane] = exp2f((float)(__shfl(x, 63) - x));
+            c[2 * kC + lane] = b;
+            if constexpr (BACK) a.gam[val * kC + lane] = x;
+        }
+        __syncthreads();
+        // Y to ts, L to xs: this wave's row tile; the tile right of an even diagonal one is zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j > (wv | 1)) continue;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * wv + 4 * q4 + r, c = 16 * j + n;
+                const float d = c <= i ? exp2f((float)(gam[i] - gam[c])) : 0.f;
+                ts[i][c] = c <= i ? d * qk[j][r] : 0.f;
+                xs[i][c] = c < i ? d * kk[j][r] : 0.f;
+            }
+        }
+        __syncthreads();
+        if constexpr (BACK)
+            up(ts, a.yt + val * kSum * kTriFrags * kFrag);
+        else
+            low(ts, a.ym + val * R * kTriFrags * kFrag, std::integral_constant<int, R>());
+        __syncthreads();
+        // M's diagonal blocks, row by row: M_i = sum_(j<i) L_ij T_j, T_i = e_i - beta_i M_i; lane
+        // (n, q) has column n of block q
+        if (wv == 0) {
+            float t[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float m = 0.f;
+#pragma unroll
+                for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(&xs[16 * q4 + i][16 * q4 + 4 * j4]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (4 * j4 + j < i) m += x[j] * t[4 * j4 + j];
+                }
+                t[i] = (i == n ? 1.f : 0.f) - bet[16 * q4 + i] * m;
+                ts[16 * q4 + i][16 * q4 + n] = m;
+            }
+        }
+        __syncthreads();
+        // the blocks below, a block diagonal at a time: with A = sum_(j<=k<i) L_ik T_kj,
+        // M_ij = (I - M_ii beta) A.  Contraction step r of a 16 x 16 product takes indexes
+        // 4 q + r, which is how accumulators lie.
+#pragma unroll
+        for (int d = 1; d < 4; ++d) {
+            if (wv >= d) {
+                const int j = wv - d;
+                f32x4 acc = {0, 0, 0, 0};
+                for (int k = j; k < wv; ++k) {
+                    const f32x4 x = *reinterpret_cast<const f32x4*>(&xs[row][16 * k + 4 * q4]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int kk_ = 4 * q4 + r;
+                        const float t = (k == j && kk_ == n ? 1.f : 0.f) - bet[16 * k + kk_] * ts[16 * k + kk_][16 * j + n];
+                        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r], t, acc, 0, 0, 0);
+                    }
+                }
+                const f32x4 m = *reinterpret_cast<const f32x4*>(&ts[row][16 * wv + 4 * q4]);
+                f32x4 out = acc;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    out = __builtin_amdgcn_mfma_f32_16x16x4f32(-m[r], bet[16 * wv + 4 * q4 + r] * acc[r], out, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ts[16 * wv + 4 * q4 + r][16 * j + n] = out[r];
+            }
+            __syncthreads();
+        }
+        low(ts, a.tm + val * kSum * kTriFrags * kFrag, std::integral_constant<int, kSum>());
+        if constexpr (BACK) up(ts, a.tt + val * kSum * kTriFrags * kFrag);
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ scan
+//
+// One workgroup per (sequence, value head, slice of 16 NC value columns), d_k / 32 waves.  Wave w
+// keeps rows 32 w .. 32 w + 31 of the slice of H in accumulators (fp32), which are one contraction
+// step of K H and Q H: each wave forms its part of those products from registers alone, the parts
+// meet in LDS, and then row tile i of the chunk (16 rows) is worked on by wave i.  Operands of a
+// chunk are requested while the chunk before it is worked on.
+// BACK: instead of the outputs, the state before each chunk and W are kept for the gradients.
+template <int IO, int DK>
+__device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b, int& hv, int& sl) {
+    // Workgroups go to the eight XCDs in turn: the slices of a head stay on one, whose L2 they share.
+    const int heads = a.B * a.Hv, blk = blockIdx.x;
+    const int whole = heads / 8 * 8 * slices;
+    int head;
+    if (blk < whole) {
+        head = blk / (8 * slices) * 8 + blk % 8;
+        sl = blk / 8 % slices;
+    } else {
+        head = heads / 8 * 8 + (blk - whole) / slices;
+        sl = (blk - whole) % slices;
+    }
+    b = head / a.Hv;
+    hv = head - b * a.Hv;
+}
+
+template <int IO, int DK, int NC, bool BACK>
+__global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
+    constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
+    constexpr int NI = NW < 4 ? 4 / NW : 1;          // row tiles of a wave (waves past the fourth have none)
+    constexpr int S = kSum, R = kRound<IO>;
+    constexpr int Y = BACK ? 1 : 2;                  // products that meet in LDS: K H, and Q H
+    __shared__ f32x4 part[Y][NW][4][NC][64];
+    __shared__ __attribute__((aligned(16))) uint16_t rr[S][NC * 16][kTp], uu[R][NC * 16][kTp], ue[S][NC * 16][kTp];
+
+    int b, hv, sl;
+    scan_place<IO, DK>(a, a.dvp / (16 * NC), b, hv, sl);
+    const int hk = hv / a.group;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const RuleSeq seq = rule_seq(a, b);
+    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
+    const int col0 = sl * 16 * NC + n;               // this lane's columns: col0 + 16 c
+    constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
+    constexpr size_t kTri = (size_t)kTriFrags * kFrag;
+
+    // H: rows 32 wv + 16 t + 4 q4 + r, columns col0 + 16 c
+    f32x4 h[2][NC];
+    const size_t state = ((size_t)b * a.Hv + hv) * a.dv * a.dk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 32 * wv + 16 * t + 4 * q4 + r, j = col0 + 16 * c;
+                h[t][c][r] = a.S0 && i < a.dk && j < a.dv ? a.S0[state + (size_t)j * a.dk + i] : 0.f;
+            }
+
+    struct Next {
+        bf16x8 kf[4][P], kt[2][2][P];
+        bf16x8 qf[BACK ? 1 : 4][P], tm[NI][2][S], ym[BACK ? 1 : NI][2][R];
+        f32x4 ca[NI], ce[NI], cb[NI], v[NI][NC];
+        float end;
+    };
+    auto load = [&](int c, Next& x) {
+        const size_t key = ((size_t)(base + c) * a.Hk + hk) * kTile, val = (size_t)(base + c) * a.Hv + hv;
+        const float* co = a.coef + val * 3 * kC;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                x.kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+                if constexpr (!BACK) x.qf[i][p] = load_frag(a.qf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+            }
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+            x.ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
+            x.ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
+            x.cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s > i / 2) continue;
+#pragma unroll
+                for (int p = 0; p < S; ++p)
+                    x.tm[ii][s][p] = load_frag(a.tm + (val * S + p) * kTri + low_frag(i, s) * kFrag, lane);
+                if constexpr (!BACK)
+#pragma unroll
+                    for (int p = 0; p < R; ++p)
+                        x.ym[ii][s][p] = load_frag(a.ym + (val * R + p) * kTri + low_frag(i, s) * kFrag, lane);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = c * kC + 16 * i + 4 * q4 + r;
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) {
+                    const int col = col0 + 16 * cc;
+                    const bool in = row < seq.n && col < a.dv;
+                    x.v[ii][cc][r] = in ? ld_io<IO>(a.v.p, (size_t)((seq.row0 + row) * a.v.row + hv * a.v.head + col)) : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    x.kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+        x.end = co[kC - 1];
+    };
+
+    Next x;
+    if (P == 1 && chunks > 0) load(0, x);
+    for (int c = 0; c < chunks; ++c) {
+        if constexpr (P > 1) load(c, x);             // registers do not hold two chunks' operands
+        Next nx;
+        if (P == 1 && c + 1 < chunks) load(c + 1, nx);
+        const size_t val = (size_t)(base + c) * a.Hv + hv;
+        // parts of K H and Q H
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            bf16x8 hb[S];
+            s16x4 h0[S], h1[S];
+            split4p(h[0][cc], h0);
+            split4p(h[1][cc], h1);
+#pragma unroll
+            for (int p = 0; p < S; ++p) hb[p] = stack_pair(h0[p], h1[p]);
+            if constexpr (BACK) {                    // the state before the chunk, for the gradients
+                float* to = a.ht + val * DK * a.dvp + col0 + 16 * cc;
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = h[t][cc][r];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                part[0][wv][i][cc][lane] = mma<P, S>(x.kf[i], hb, f32x4{0, 0, 0, 0});
+                if constexpr (!BACK) part[Y - 1][wv][i][cc][lane] = mma<P, R>(x.qf[i], hb, f32x4{0, 0, 0, 0});
+            }
+        }
+        lds_barrier();
+        f32x4 qh[NI][NC], f[NI][NC];
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                f32x4 s = part[0][0][i][cc][lane];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) s += part[0][w][i][cc][lane];
+                f[ii][cc] = x.v[ii][cc] - x.ca[ii] * s;
+                put4<S>(&rr[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, x.cb[ii] * f[ii][cc]);
+                if constexpr (!BACK) {
+                    s = part[Y - 1][0][i][cc][lane];
+#pragma unroll
+                    for (int w = 1; w < NW; ++w) s += part[Y - 1][w][i][cc][lane];
+                    qh[ii][cc] = x.ca[ii] * s;
+                }
+            }
+        }
+        lds_barrier();
+        // W = F - M R, U = beta W
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                f32x4 m = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s > i / 2) continue;
+                    bf16x8 r[S];
+                    get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, r);
+                    m = mma<S, S>(x.tm[ii][s], r, m);
+                }
+                const f32x4 w = f[ii][cc] - m, u = x.cb[ii] * w;
+                put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, x.ce[ii] * u);
+                if constexpr (BACK) {
+                    float* to = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) to[(size_t)r * a.dvp] = w[r];
+                } else {
+                    put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, u);
+                }
+            }
+        }
+        lds_barrier();
+        // H' and the outputs
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            bf16x8 u[2][S];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) get8<S>(&ue[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, u[s]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                h[t][cc] = x.end * h[t][cc];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) h[t][cc] = mma<P, S>(x.kt[t][s], u[s], h[t][cc]);
+            }
+        }
+        if constexpr (!BACK) {
+#pragma unroll
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = wv + ii * NW;
+                if (i >= 4) break;
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) {
+                    f32x4 o = qh[ii][cc];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (s > i / 2) continue;
+                        bf16x8 u[R];
+                        get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, u);
+                        o = mma<R, R>(x.ym[ii][s], u, o);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
+                        if (row < seq.n && col < a.dv)
+                            st_io<IO>(a.o.p, (size_t)((seq.row0 + row) * a.o.row + hv * a.o.head + col), o[r]);
+                    }
+                }
+            }
+        }
+        if (P == 1 && c + 1 < chunks) x = nx;
+    }
+    if (!BACK && a.S_out) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 32 * wv + 16 * t + 4 * q4 + r, j = col0 + 16 * cc;
+                    if (i < a.dk && j < a.dv) a.S_out[state + (size_t)j * a.dk + i] = h[t][cc][r];
+                }
+    }
+}
+
+// ------------------------------------------------------------------ scan_back
+
+// Sum over the 16 lanes of a row, in every lane.
+__device__ __forceinline__ float row_sum(float x) {
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x128, 0xf, 0xf, false));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x124, 0xf, 0xf, false));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x122, 0xf, 0xf, false));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x121, 0xf, 0xf, false));
+    return x;
+}
+
+// Sums of the lanes up to each within a row of 16.
+__device__ __forceinline__ float row_scan(float x) {
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x111, 0xf, 0xf, true));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x112, 0xf, 0xf, true));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x114, 0xf, 0xf, true));
+    x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x118, 0xf, 0xf, true));
+    return x;
+}
+
+// rule_scan's shape from the last chunk to the first, the accumulators holding the slice of dH.
+// It leaves dH' and dR of every chunk for rule_join, writes dV, and leaves the slice's parts of
+// dbeta and of the terms of d ln g that reach the chunk's end: e^(Gamma_C - Gamma_j) k_j . dH' u_j
+// of every row, and a_C <H, dH'>.
+template <int IO, int DK, int NC>
+__global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
+    constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
+    constexpr int NI = NW < 4 ? 4 / NW : 1;
+    constexpr int S = kSum;
+    constexpr int kPl = NC * 16 * kTp;               // elements of a plane of a [column][row] tile
+    __shared__ f32x4 part[NW][4][NC][64];
+    __shared__ __attribute__((aligned(16))) uint16_t od[P][NC * 16][kTp], oa[S][NC * 16][kTp], ou[S][NC * 16][kTp],
+        oz[S][NC * 16][kTp];
+
+    int b, hv, sl;
+    const int slices = a.dvp / (16 * NC);
+    scan_place<IO, DK>(a, slices, b, hv, sl);
+    const int hk = hv / a.group;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const RuleSeq seq = rule_seq(a, b);
+    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
+    const int col0 = sl * 16 * NC + n;
+    constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
+    constexpr size_t kTri = (size_t)kTriFrags * kFrag;
+
+    f32x4 dh[2][NC];
+    const size_t state = ((size_t)b * a.Hv + hv) * a.dv * a.dk;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 32 * wv + 16 * t + 4 * q4 + r, j = col0 + 16 * c;
+                dh[t][c][r] = a.dS_out && i < a.dk && j < a.dv ? a.dS_out[state + (size_t)j * a.dk + i] : 0.f;
+            }
+
+    struct Next {
+        bf16x8 kf[4][P], kt[2][2][P], qt[2][2][P], tt[NI][2][S], yt[NI][2][S];
+        f32x4 ca[NI], ce[NI], cb[NI], d_o[NI][NC], w[NI][NC], h[2][NC];
+        float end;
+    };
+    auto load = [&](int c, Next& x) {
+        const size_t key = ((size_t)(base + c) * a.Hk + hk) * kTile, val = (size_t)(base + c) * a.Hv + hv;
+        const float* co = a.coef + val * 3 * kC;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) x.kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+            x.ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
+            x.ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
+            x.cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s < i / 2) continue;
+#pragma unroll
+                for (int p = 0; p < S; ++p) {
+                    x.tt[ii][s][p] = load_frag(a.tt + (val * S + p) * kTri + up_frag(i, s) * kFrag, lane);
+                    x.yt[ii][s][p] = load_frag(a.yt + (val * S + p) * kTri + up_frag(i, s) * kFrag, lane);
+                }
+            }
+            const float* w = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = c * kC + 16 * i + 4 * q4 + r;
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) {
+                    const int col = col0 + 16 * cc;
+                    const bool in = row < seq.n && col < a.dv;
+                    x.d_o[ii][cc][r] =
+                        in ? ld_io<IO>(a.d_o.p, (size_t)((seq.row0 + row) * a.d_o.row + hv * a.d_o.head + col)) : 0.f;
+                    x.w[ii][cc][r] = w[(size_t)r * a.dvp + 16 * cc];
+                }
+            }
+        }
+        const float* h = a.ht + (val * DK + 32 * wv + 4 * q4) * a.dvp + col0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    x.kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+                    x.qt[t][s][p] = load_frag(a.qt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+                }
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x.h[t][cc][r] = h[(size_t)(16 * t + r) * a.dvp + 16 * cc];
+        }
+        x.end = co[kC - 1];
+    };
+
+    Next x;
+    if (P == 1 && chunks > 0) load(chunks - 1, x);
+    for (int c = chunks - 1; c >= 0; --c) {
+        if constexpr (P > 1) load(c, x);
+        Next nx;
+        if (P == 1 && c > 0) load(c - 1, nx);
+        const size_t val = (size_t)(base + c) * a.Hv + hv;
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, x.d_o[ii][cc]);
+        }
+        // parts of K dH', and a_C <H, dH'>
+        float pa = 0.f;
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            bf16x8 hb[S];
+            s16x4 h0[S], h1[S];
+            split4p(dh[0][cc], h0);
+            split4p(dh[1][cc], h1);
+#pragma unroll
+            for (int p = 0; p < S; ++p) hb[p] = stack_pair(h0[p], h1[p]);
+            float* to = a.dht + val * DK * a.dvp + col0 + 16 * cc;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = dh[t][cc][r];
+                    pa += x.h[t][cc][r] * dh[t][cc][r];
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[wv][i][cc][lane] = mma<P, S>(x.kf[i], hb, f32x4{0, 0, 0, 0});
+        }
+        pa = row_sum(x.end * pa);
+        if (n == 0) a.pa[((val * slices + sl) * NW + wv) * 4 + q4] = pa;
+        lds_barrier();
+        f32x4 du[NI][NC], pe[NI];
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                f32x4 s = part[0][i][cc][lane];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) s += part[w][i][cc][lane];
+                s *= x.ce[ii];
+                pe[ii] = (cc ? pe[ii] : f32x4{0, 0, 0, 0}) + s * x.cb[ii] * x.w[ii][cc];
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    if (st < i / 2) continue;
+                    bf16x8 d[P];
+                    get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
+                    s = mma<S, P>(x.yt[ii][st], d, s);
+                }
+                du[ii][cc] = s;
+                put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, x.cb[ii] * s);
+                put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, x.ca[ii] * x.d_o[ii][cc]);
+            }
+        }
+        lds_barrier();
+        // dR = dU - M^T beta dU
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = wv + ii * NW;
+            if (i >= 4) break;
+            f32x4 pb = {0, 0, 0, 0};
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc) {
+                f32x4 m = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    if (s < i / 2) continue;
+                    bf16x8 u[S];
+                    get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                    m = mma<S, S>(x.tt[ii][s], u, m);
+                }
+                const f32x4 dr = du[ii][cc] - m, dv = x.cb[ii] * dr;
+                put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -x.ca[ii] * dv);
+                float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
+                    to[(size_t)r * a.dvp] = dr[r];
+                    if (row < seq.n && col < a.dv)
+                        st_io<IO>(a.dv_out.p, (size_t)((seq.row0 + row) * a.dv_out.row + hv * a.dv_out.head + col), dv[r]);
+                }
+                pb += dr * x.w[ii][cc];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pb[r] = row_sum(pb[r]), pe[ii][r] = row_sum(pe[ii][r]);
+            if (n == 0) {
+                const size_t at = (val * slices + sl) * kC + 16 * i + 4 * q4;
+                *reinterpret_cast<f32x4*>(a.pb + at) = pb;
+                *reinterpret_cast<f32x4*>(a.pe + at) = pe[ii];
+            }
+        }
+        lds_barrier();
+        // dH
+#pragma unroll
+        for (int cc = 0; cc < NC; ++cc) {
+            bf16x8 u[2][S], z[2][S];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                get8<S>(&oa[0][16 * cc + n][32 * s + 8 * q4], kPl, u[s]);
+                get8<S>(&oz[0][16 * cc + n][32 * s + 8 * q4], kPl, z[s]);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                dh[t][cc] = x.end * dh[t][cc];
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    dh[t][cc] = mma<P, S>(x.qt[t][s], u[s], dh[t][cc]);
+                    dh[t][cc] = mma<P, S>(x.kt[t][s], z[s], dh[t][cc]);
+                }
+            }
+        }
+        if (P == 1 && c > 0) x = nx;
+    }
+    if (a.dS0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 32 * wv + 16 * t + 4 * q4 + r, j = col0 + 16 * cc;
+                    if (i < a.dk && j < a.dv) a.dS0[state + (size_t)j * a.dk + i] = dh[t][cc][r];
+                }
+    }
+}
+
+// ------------------------------------------------------------------ join
+//
+// dQ, dK and the gates' gradients, one workgroup per (chunk slot, key head) and d_k / 16 waves:
+// wave w owns columns 16 w .. 16 w + 15 of dQ and dK and sums them over the key head's value
+// heads in registers, so that gradients of shared heads need no atomics.  The 16 x 16 tiles of
+// dO U^T and dR U^T below the diagonal are dealt to the waves; value columns go by blocks of 128.
+//
+// d ln g_t is the sum of what every path across row t carries, a path from row j or from the
+// chunk's start to row i or to the chunk's end:
+//
+//     sum_(i >= t > j) Z_ij + sum_(i >= t) h_i + sum_(j < t) e_j + a_C <H, dH'>,
+//     Z = P o Q K^T + G o K K^T,  h_i = a_i (dO_i . H^T q_i - beta_i dR_i . H^T k_i)
+//
+// A running sum of differences over the rows (v . dv - o . do) would be shorter, but its terms do
+// not shrink with the gate: a head that forgets at once would get its small gradient as a
+// difference of large ones.
+template <int IO, int DK>
+__global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int slices) {
+    constexpr int P = kPlanes<IO>, KS = DK / 32, NT = DK / 16, NW = NT, VB = 128, LD = VB + 8;
+    constexpr int S = kSum, R = kRound<IO>, D = R;  // D: terms of dH', P^T and G in dK
+    constexpr int kPl = kC * LD, kSq = kC * kTp;
+    constexpr int ND = (10 + NW - 1) / NW;           // tiles below or on the diagonal, per wave
+    constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
+    // value rows; then, in the same place, the 64 x 64 matrices
+    __shared__ __attribute__((aligned(16))) uint16_t lds[(2 * S + P) * kPl];
+    static_assert((2 * S + P) * kPl >= (S + 2 * D) * kSq, "the matrices fit");
+    __shared__ double gam[kC];
+    __shared__ float coef[3][kC];
+    __shared__ float hs[NW][kC];                     // parts of h
+    __shared__ float zc[10][16], zr[10][16];         // of a tile of Z: what its row t crosses, its row sums
+    uint16_t *su = lds, *sr = lds + S * kPl, *so = sr + S * kPl;
+    uint16_t *sp = lds, *spt = lds + S * kSq, *sg = spt + D * kSq;
+
+    const int slot = blockIdx.x, hk = blockIdx.y;
+    const RuleChunk ch = rule_chunk(a, slot);
+    if (ch.n == 0) return;
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const size_t key = ((size_t)slot * a.Hk + hk) * kTile;
+    const int col = 16 * wv + n;
+
+    f32x4 dq[4], dk[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0, 0, 0, 0};
+    auto tile_row = [](int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; };
+    auto tile_col = [&](int t) { return t - tile_row(t) * (tile_row(t) + 1) / 2; };
+    // K K^T and Q K^T, for Z
+    f32x4 kk[ND], qk[ND];
+#pragma unroll
+    for (int x = 0; x < ND; ++x) {
+        const int t = wv + x * NW;
+        kk[x] = qk[x] = f32x4{0, 0, 0, 0};
+        if (t >= 10) break;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            bf16x8 k[P], q[P], b[P];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                k[p] = load_frag(a.kf + key + ((p * 4 + tile_row(t)) * KS + s) * kFrag, lane);
+                q[p] = load_frag(a.qf + key + ((p * 4 + tile_row(t)) * KS + s) * kFrag, lane);
+                b[p] = load_frag(a.kf + key + ((p * 4 + tile_col(t)) * KS + s) * kFrag, lane);
+            }
+            kk[x] = mma<P, P>(k, b, kk[x]);
+            qk[x] = mma<P, P>(q, b, qk[x]);
+        }
+    }
+
+    for (int gi = 0; gi < a.group; ++gi) {
+        const int hv = hk * a.group + gi;
+        const size_t val = (size_t)slot * a.Hv + hv;
+        f32x4 dy[ND], dx[ND], aq[4], t1[4], t2[4];
+#pragma unroll
+        for (int i = 0; i < ND; ++i) dy[i] = dx[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) aq[i] = t1[i] = t2[i] = f32x4{0, 0, 0, 0};
+
+        for (int v0 = 0; v0 < a.dvp; v0 += VB) {
+            const int width = min(VB, a.dvp - v0), pieces = width / 8;
+            __syncthreads();
+            if (v0 == 0 && tid < kC) {
+                gam[tid] = a.gam[val * kC + tid];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) coef[x][tid] = a.coef[(val * 3 + x) * kC + tid];
+            }
+            for (int p = tid; p < kC * pieces; p += NW * 64) {
+                const int r = p / pieces, c = (p - r * pieces) * 8;
+                const size_t at = (val * kC + r) * a.dvp + v0 + c;
+                const float beta = a.coef[(val * 3 + 2) * kC + r];
+                float u[8], d[8];
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(a.w + at + j);
+                    const f32x4 y = *reinterpret_cast<const f32x4*>(a.dr + at + j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) u[j + k] = beta * w[k], d[j + k] = y[k];
+                }
+                bf16x8 us[S], ds[S];
+                split8(u, us);
+                split8(d, ds);
+#pragma unroll
+                for (int x = 0; x < S; ++x) {
+                    *reinterpret_cast<bf16x8*>(su + x * kPl + r * LD + c) = us[x];
+                    *reinterpret_cast<bf16x8*>(sr + x * kPl + r * LD + c) = ds[x];
+                }
+                const bool live = r < ch.n;
+                const Planes<IO> o = load_row8<IO>(a.d_o.p, (ch.row0 + (live ? r : 0)) * a.d_o.row + (int64_t)hv * a.d_o.head,
+                                                   v0 + c, a.dv, a.vdo, live);
+#pragma unroll
+                for (int x = 0; x < P; ++x) *reinterpret_cast<bf16x8*>(so + x * kPl + r * LD + c) = o.p[x];
+            }
+            __syncthreads();
+            for (int s = 0; s < width / 32; ++s) {
+                const int at = 32 * s + 8 * q4;
+                // dO U^T and dR U^T
+#pragma unroll
+                for (int x = 0; x < ND; ++x) {
+                    const int t = wv + x * NW;
+                    if (t >= 10) break;
+                    const int i = tile_row(t), j = tile_col(t);
+                    bf16x8 u[S], o[P], r[S];
+                    get8<S>(su + (16 * j + n) * LD + at, kPl, u);
+                    get8<P>(so + (16 * i + n) * LD + at, kPl, o);
+                    get8<S>(sr + (16 * i + n) * LD + at, kPl, r);
+                    dy[x] = mma<P, S>(o, u, dy[x]);
+                    dx[x] = mma<S, S>(r, u, dx[x]);
+                }
+                // dO H^T, dR H^T and U dH'^T
+                float x[8], y[8];
+                const size_t st = (val * DK + col) * a.dvp + v0 + at;
+#pragma unroll
+                for (int j = 0; j < 8; j += 4) {
+                    const f32x4 u = *reinterpret_cast<const f32x4*>(a.ht + st + j);
+                    const f32x4 w = *reinterpret_cast<const f32x4*>(a.dht + st + j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[j + k] = u[k], y[j + k] = w[k];
+                }
+                bf16x8 h[S], d[D];
+                split8(x, h);
+                split8(y, d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    bf16x8 u[R], o[P], r[S];
+                    get8<R>(su + (16 * i + n) * LD + at, kPl, u);
+                    get8<P>(so + (16 * i + n) * LD + at, kPl, o);
+                    get8<S>(sr + (16 * i + n) * LD + at, kPl, r);
+                    aq[i] = mma<P, S>(o, h, aq[i]);
+                    t2[i] = mma<S, S>(r, h, t2[i]);
+                    t1[i] = mma<R, D>(u, d, t1[i]);
+                }
+            }
+        }
+        __syncthreads();
+        // P, its transpose, G + G^T, and the sums of Z
+#pragma unroll
+        for (int x = 0; x < ND; ++x) {
+            const int t = wv + x * NW;
+            if (t >= 10) break;
+            const int i = tile_row(t), j = tile_col(t);
+            f32x4 p, g;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * q4 + r, c = 16 * j + n;
+                const float d = c <= row ? exp2f((float)(gam[row] - gam[c])) : 0.f;
+                p[r] = c <= row ? d * dy[x][r] : 0.f;
+                g[r] = c < row ? -coef[2][row] * d * dx[x][r] : 0.f;
+            }
+            // z: the sums of Z's columns up to this one; of column 15, of the whole row.  Row t = 16 j + n + 1
+            // is crossed by the rows i >= t of them.
+            float cross = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 4 * q4 + r;
+                const float z = row_scan(i == j && n == row ? 0.f : p[r] * qk[x][r] + g[r] * kk[x][r]);
+                if (n == 15) zr[t][row] = z;
+                if (i > j || row > n) cross += z;
+            }
+            cross += __shfl_xor(cross, 16);
+            cross += __shfl_xor(cross, 32);
+            if (q4 == 0 && n < 15) zc[t][n + 1] = cross;
+            if (lane == 0) zc[t][0] = 0.f;
+            s16x4 ps[S], gs[D];
+            split4p(p, ps);
+            split4p(g, gs);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * q4 + r, c = 16 * j + n;
+#pragma unroll
+                for (int y = 0; y < S; ++y) sp[y * kSq + row * kTp + c] = (uint16_t)ps[y][r];
+#pragma unroll
+                for (int y = 0; y < D; ++y) {        // on the diagonal block the upper half comes from below
+                    if (c <= row) sg[y * kSq + row * kTp + c] = (uint16_t)gs[y][r];
+                    if (c < row) sg[y * kSq + c * kTp + row] = (uint16_t)gs[y][r];
+                }
+                if (i == j && (i & 1) == 0) {        // the zero tile that shares an operand with this one
+#pragma unroll
+                    for (int y = 0; y < S; ++y) sp[y * kSq + row * kTp + c + 16] = 0;
+#pragma unroll
+                    for (int y = 0; y < D; ++y) spt[y * kSq + (row + 16) * kTp + c] = 0;
+                }
+            }
+            put4<D>(spt + (16 * j + n) * kTp + 16 * i + 4 * q4, kSq, p);
+        }
+        __syncthreads();
+        bf16x8 kt[2][P], qt[2][P];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                kt[s][p] = load_frag(a.kt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
+                qt[s][p] = load_frag(a.qt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 ca = *reinterpret_cast<const f32x4*>(&coef[0][16 * i + 4 * q4]);
+            const f32x4 ce = *reinterpret_cast<const f32x4*>(&coef[1][16 * i + 4 * q4]);
+            const f32x4 cb = *reinterpret_cast<const f32x4*>(&coef[2][16 * i + 4 * q4]);
+            f32x4 xq = ca * aq[i], xk = ce * t1[i] - ca * cb * t2[i];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * q4 + r;
+                const bool in = row < ch.n && col < a.dk;
+                const float q = in ? ld_io<IO>(a.q.p, (size_t)((ch.row0 + row) * a.q.row + hk * a.q.head + col)) : 0.f;
+                const float k = in ? ld_io<IO>(a.k.p, (size_t)((ch.row0 + row) * a.k.row + hk * a.k.head + col)) : 0.f;
+                const float x = row_sum(q * xq[r] - k * ca[r] * cb[r] * t2[i][r]);
+                if (n == 0) hs[wv][row] = x;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int at = (16 * i + n) * kTp + 32 * s + 8 * q4;
+                bf16x8 m[S], g[D];
+                if (s <= i / 2) {
+                    get8<S>(sp + at, kSq, m);
+                    xq = mma<S, P>(m, kt[s], xq);
+                }
+                if (s >= i / 2) {
+                    get8<D>(spt + at, kSq, g);
+                    xk = mma<D, P>(g, qt[s], xk);
+                }
+                get8<D>(sg + at, kSq, g);
+                xk = mma<D, P>(g, kt[s], xk);
+            }
+            dq[i] += xq;
+            dk[i] += xk;
+        }
+        __syncthreads();
+        if (wv == 0) {
+            const size_t at0 = val * slices;
+            double own = 0, to_end = 0, lead = 0;
+            float db = 0;
+            for (int w = 0; w < NW; ++w) own += hs[w][lane];
+            for (int s = 0; s < slices; ++s) {
+                to_end += a.pe[(at0 + s) * kC + lane];
+                db += a.pb[(at0 + s) * kC + lane];
+            }
+            for (int s = lane; s < slices * KS * 4; s += 64) lead += a.pa[at0 * KS * 4 + s];
+            const double mine = to_end;
+#pragma unroll
+            for (int off = 1; off < 64; off *= 2) {
+                const double y = __shfl_down(own, off), z = __shfl_up(to_end, off);
+                if (lane + off < 64) own += y;
+                if (lane >= off) to_end += z;
+                lead += __shfl_xor(lead, off);
+            }
+            double d = lead + own + to_end - mine;
+            const int T = q4;                        // row t = 16 T + n
+            for (int t = 0; t < 10; ++t) {
+                const int i = tile_row(t), j = tile_col(t);
+                if (j == T) d += zc[t][n];
+                if (j < T && T <= i)
+                    for (int r = T == i ? n : 0; r < 16; ++r) d += zr[t][r];
+            }
+            if (lane < ch.n) {
+                const int64_t at = (ch.row0 + lane) * a.Hv + hv;
+                a.dlog_g[at] = (float)d;
+                a.dbeta[at] = db;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * i + 4 * q4 + r;
+            if (row < ch.n && col < a.dk) {
+                st_io<IO>(a.dq.p, (size_t)((ch.row0 + row) * a.dq.row + hk * a.dq.head + col), dq[i][r]);
+                st_io<IO>(a.dk_out.p, (size_t)((ch.row0 + row) * a.dk_out.row + hk * a.dk_out.head + col), dk[i][r]);
+            }
+        }
+}
+
+// ------------------------------------------------------------------ launchers
+
+template <int IO, int DK>
+hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
+    constexpr int NC = 1;
+    hipError_t e = hipSuccess;
+    if (a.T > 0)
+        e = launch(rule_prepare<IO, DK, false>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
+    if (e != hipSuccess) return e;
+    return launch(rule_scan<IO, DK, NC, false>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))), dim3(DK * 2), 0, stream, a);
+}
+
+template <int IO, int DK>
+hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
+    constexpr int NC = 1;
+    const int slices = a.dvp / (16 * NC);
+    hipError_t e = hipSuccess;
+    if (a.T > 0) {
+        e = launch(rule_prepare<IO, DK, true>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
+        if (e == hipSuccess)
+            e = launch(rule_scan<IO, DK, NC, true>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
+    }
+    if (e == hipSuccess)
+        e = launch(rule_scan_back<IO, DK, NC>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
+    if (e == hipSuccess && a.T > 0)
+        e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a, slices);
+    return e;
+}
+
+}  // namespace gdn
