@@ -1,8 +1,8 @@
 """Python binding of libgdntree.so: rollback-free GDN draft-tree verification on
 MI355X (gfx950).
 
-The names mirror the C ABI in include/gdn_tree.h, gdn_attn.h and gdn_rule.h.  This module only marshals
-arguments: it checks that each torch tensor has the shape, dtype and
+The names mirror the C ABI in include/gdn_tree.h, gdn_attn.h, gdn_rule.h and gdn_score.h.  This module only
+marshals arguments: it checks that each torch tensor has the shape, dtype and
 contiguity the C ABI documents (so a kernel never reads past a buffer) and
 passes device pointers and the current HIP stream.  Every step of the
 computation runs in the library's HIP kernels; there is no other path.  PyTorch
@@ -28,6 +28,8 @@ __all__ = [
     "gdn_pages_copy", "gdn_pages_free", "gdn_pages_compact",
     "RuleDims", "rule_dims", "rule_workspace", "gdn_rule_workspace_bytes", "gdn_rule_forward",
     "gdn_rule_backward", "gdn_rule_step",
+    "ScoreDims", "score_dims", "score_workspace", "gdn_score_workspace_bytes", "gdn_token_scores",
+    "gdn_token_scores_backward",
 ]
 
 GDN_F32, GDN_BF16 = 0, 1
@@ -793,3 +795,79 @@ def gdn_rule_step(d: RuleDims, q, k, v, beta, g, state, o, slot=None, stream=Non
           _attn_rows(v, B, d.h_v, d.d_v, io, "v"), gate(beta, "beta"), gate(g, "g"),
           _ptr(state, (n, d.h_v, d.d_v, d.d_k), torch.float32, "state"), _attn_rows(o, B, d.h_v, d.d_v, io, "o"),
           _stream(stream))
+
+
+# ---------------------------------------------------------------- scores of tokens
+# Log-probabilities, entropy and best alternatives of rows of logits, and their gradient
+# (include/gdn_score.h).  Logits are [rows, vocab] with the last axis contiguous.
+
+
+class ScoreDims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("row_stride", ctypes.c_int64)] + \
+        [(n, ctypes.c_int32) for n in ("vocab", "topk", "io_dtype")]
+
+
+_sd = ctypes.POINTER(ScoreDims)
+for _name, _args in {
+        "gdn_score_workspace_bytes": [_sd, _sz],
+        "gdn_token_scores": [_sd] + [_vp] * 9,
+        "gdn_token_scores_backward": [_sd] + [_vp] * 10}.items():
+    getattr(_lib, _name).argtypes = _args
+    getattr(_lib, _name).restype = _i
+
+
+def score_dims(rows, vocab, topk, io_dtype, row_stride=None) -> ScoreDims:
+    """row_stride: elements between rows of logits, vocab unless given."""
+    if isinstance(io_dtype, str):
+        io_dtype = {"f32": GDN_F32, "bf16": GDN_BF16}[io_dtype]
+    return ScoreDims(rows, vocab if row_stride is None else row_stride, vocab, topk, io_dtype)
+
+
+def gdn_score_workspace_bytes(d: ScoreDims) -> int:
+    out = ctypes.c_size_t()
+    _call("gdn_score_workspace_bytes", ctypes.byref(d), ctypes.byref(out))
+    return out.value
+
+
+def score_workspace(d: ScoreDims, device="cuda"):
+    """A workspace for gdn_token_scores of these dims.  Nothing of it lasts from call to call."""
+    return torch.empty(max(gdn_score_workspace_bytes(d), 16), dtype=torch.uint8, device=device)
+
+
+def _logits(x, d, name):
+    if x.dtype != _io_dtype(d) or not x.is_cuda:
+        raise ValueError(f"{name}: expected a device tensor of {_io_dtype(d)}")
+    if x.shape != (d.rows, d.vocab):
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, expected {(d.rows, d.vocab)}")
+    if d.rows and (x.stride(1) != 1 and d.vocab > 1 or x.stride(0) != d.row_stride and d.rows > 1):
+        raise ValueError(f"{name}: strides {x.stride()}, expected ({d.row_stride}, 1)")
+    return x.data_ptr()
+
+
+def _floats(x, shape, name):
+    return _ptr(x, shape, torch.float32, name)
+
+
+def gdn_token_scores(d: ScoreDims, logits, tokens, logp, entropy, lse, workspace, top_logp=None, top_tok=None,
+                     stream=None) -> None:
+    """Enqueue the scores of every row (see gdn_score.h).  tokens with logp, entropy, lse: None where not
+    wanted; top_logp and top_tok: [rows, topk]."""
+    n, k, need = (d.rows,), (d.rows, d.topk), gdn_score_workspace_bytes(d)
+    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() or \
+            workspace.numel() < need:
+        raise ValueError(f"workspace: expected {need} contiguous bytes or more (score_workspace)")
+    _call("gdn_token_scores", ctypes.byref(d), _logits(logits, d, "logits"), _ptr(tokens, n, _int32, "tokens"),
+          _floats(logp, n, "logp"), _floats(entropy, n, "entropy"), _floats(lse, n, "lse"),
+          _floats(top_logp, k, "top_logp"), _ptr(top_tok, k, _int32, "top_tok"), workspace.data_ptr(),
+          _stream(stream))
+
+
+def gdn_token_scores_backward(d: ScoreDims, logits, tokens, lse, entropy, d_logp, d_entropy, d_logits, top_tok=None,
+                              d_top_logp=None, stream=None) -> None:
+    """Enqueue the gradient of the logits (see gdn_score.h).  d_logp, d_entropy, d_top_logp: None where there is
+    none; d_logits may be logits."""
+    n, k = (d.rows,), (d.rows, d.topk)
+    _call("gdn_token_scores_backward", ctypes.byref(d), _logits(logits, d, "logits"),
+          _ptr(tokens, n, _int32, "tokens"), _floats(lse, n, "lse"), _floats(entropy, n, "entropy"),
+          _floats(d_logp, n, "d_logp"), _floats(d_entropy, n, "d_entropy"), _ptr(top_tok, k, _int32, "top_tok"),
+          _floats(d_top_logp, k, "d_top_logp"), _logits(d_logits, d, "d_logits"), _stream(stream))

@@ -24,7 +24,7 @@ SOURCES = ["abi.hip", "verify_generic.hip", "verify_tiled.hip", "verify_large.hi
            "attn_verify_bf16_64.hip", "attn_verify_bf16_128.hip", "attn_verify_bf16_256.hip",
            "attn_verify_f32_64.hip", "attn_verify_f32_128.hip", "attn_verify_f32_256.hip",
            "rule_abi.hip", "rule_step.hip", "rule_bf16_64.hip", "rule_bf16_128.hip", "rule_bf16_256.hip",
-           "rule_f32_64.hip", "rule_f32_128.hip", "rule_f32_256.hip"]
+           "rule_f32_64.hip", "rule_f32_128.hip", "rule_f32_256.hip", "score.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", f"-I{INCLUDE}",
