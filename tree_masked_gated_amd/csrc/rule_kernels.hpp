@@ -29,7 +29,8 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
     const int slot = blockIdx.x, hk = blockIdx.y;
     const RuleChunk ch = rule_chunk(a, slot);
     if (ch.n == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
     const int row = 16 * wv + n;                     // this lane's row of an operand tile
     const bool live = row < ch.n;
     const int64_t grow = ch.row0 + (live ? row : 0);
@@ -239,19 +240,56 @@ __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b
     hv = head - b * a.Hv;
 }
 
+// Elements of a value row, four rows of one column, as they lie in memory: requested a chunk ahead,
+// converted and masked where they are used, so that nothing waits for them before.
+template <int IO>
+struct Raw4 {
+    typedef std::conditional_t<IO == GDN_BF16, uint16_t, float> E;
+    E x[4];
+    __device__ __forceinline__ void load(const Rows& from, int64_t row0, int rows, int row, int64_t head, int col, int d) {
+        const E* p = reinterpret_cast<const E*>(from.p) + head + min(col, d - 1);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = p[(row0 + min(row + r, rows - 1)) * from.row];
+    }
+    __device__ __forceinline__ f32x4 get(int rows, int row, int col, int d) const {
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            float y;
+            if constexpr (IO == GDN_BF16) y = bf16_bits_to_f32(x[r]); else y = x[r];
+            v[r] = row + r < rows && col < d ? y : 0.f;
+        }
+        return v;
+    }
+};
+
+// Parts of a product from the waves of a workgroup, as one.
+template <int NW>
+__device__ __forceinline__ f32x4 gather(const f32x4* part, int stride) {
+    f32x4 t[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) t[w] = part[w * stride];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) t[0] += t[w];
+    return t[0];
+}
+
 template <int IO, int DK, int NC, bool BACK>
 __global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
     constexpr int NI = NW < 4 ? 4 / NW : 1;          // row tiles of a wave (waves past the fourth have none)
     constexpr int S = kSum, R = kRound<IO>;
     constexpr int Y = BACK ? 1 : 2;                  // products that meet in LDS: K H, and Q H
+    constexpr int kPl = NC * 16 * kTp;               // elements of a plane of a [column][row] tile
     __shared__ f32x4 part[Y][NW][4][NC][64];
     __shared__ __attribute__((aligned(16))) uint16_t rr[S][NC * 16][kTp], uu[R][NC * 16][kTp], ue[S][NC * 16][kTp];
 
     int b, hv, sl;
     scan_place<IO, DK>(a, a.dvp / (16 * NC), b, hv, sl);
     const int hk = hv / a.group;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
+    const bool work = NW <= 4 || wv < 4;
     const RuleSeq seq = rule_seq(a, b);
     const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
     const int col0 = sl * 16 * NC + n;               // this lane's columns: col0 + 16 c
@@ -271,68 +309,78 @@ __global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
                 h[t][c][r] = a.S0 && i < a.dk && j < a.dv ? a.S0[state + (size_t)j * a.dk + i] : 0.f;
             }
 
-    struct Next {
-        bf16x8 kf[4][P], kt[2][2][P];
-        bf16x8 qf[BACK ? 1 : 4][P], tm[NI][2][S], ym[BACK ? 1 : NI][2][R];
-        f32x4 ca[NI], ce[NI], cb[NI], v[NI][NC];
-        float end;
-    };
-    auto load = [&](int c, Next& x) {
-        const size_t key = ((size_t)(base + c) * a.Hk + hk) * kTile, val = (size_t)(base + c) * a.Hv + hv;
-        const float* co = a.coef + val * 3 * kC;
+    // The operands of a chunk are requested for the next one as soon as they have been used.  No
+    // request is conditional: the compiler could not count the ones in flight, and would wait for all.
+    bf16x8 kf[4][P], qf[BACK ? 1 : 4][P], tm[NI][2][S], ym[BACK ? 1 : NI][2][R], kt[2][2][P];
+    f32x4 ca[NI], ce[NI], cb[NI];
+    Raw4<IO> v[NI][NC];
+    float end;
+    auto tile_of = [&](int ii) { return NW <= 4 ? wv + ii * NW : min(wv, 3); };
+    auto key_of = [&](int c) { return ((size_t)(base + c) * a.Hk + hk) * kTile; };
+    auto val_of = [&](int c) { return (size_t)(base + c) * a.Hv + hv; };
+    auto load_a = [&](int c) {
+        const size_t key = key_of(c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                x.kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
-                if constexpr (!BACK) x.qf[i][p] = load_frag(a.qf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+                kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+                if constexpr (!BACK) qf[i][p] = load_frag(a.qf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
             }
+    };
+    auto load_v = [&](int c) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+                v[ii][cc].load(a.v, seq.row0, seq.n, c * kC + 16 * tile_of(ii) + 4 * q4, hv * a.v.head, col0 + 16 * cc, a.dv);
+    };
+    auto load_c = [&](int c) {
+        const size_t val = val_of(c);
+        const float* co = a.coef + val * 3 * kC;
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
-            x.ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
-            x.ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
-            x.cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+            const int i = tile_of(ii);
+            ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
+            ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
+            cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s > i / 2) continue;
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < S; ++p)
-                    x.tm[ii][s][p] = load_frag(a.tm + (val * S + p) * kTri + low_frag(i, s) * kFrag, lane);
-                if constexpr (!BACK)
-#pragma unroll
-                    for (int p = 0; p < R; ++p)
-                        x.ym[ii][s][p] = load_frag(a.ym + (val * R + p) * kTri + low_frag(i, s) * kFrag, lane);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = c * kC + 16 * i + 4 * q4 + r;
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    const int col = col0 + 16 * cc;
-                    const bool in = row < seq.n && col < a.dv;
-                    x.v[ii][cc][r] = in ? ld_io<IO>(a.v.p, (size_t)((seq.row0 + row) * a.v.row + hv * a.v.head + col)) : 0.f;
-                }
-            }
+                    tm[ii][s][p] = load_frag(a.tm + (val * S + p) * kTri + low_frag(i, min(s, i / 2)) * kFrag, lane);
         }
+    };
+    auto load_d = [&](int c) {
+        const size_t key = key_of(c), val = val_of(c);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < P; ++p)
-                    x.kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
-        x.end = co[kC - 1];
+                    kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+        end = a.coef[val * 3 * kC + kC - 1];
+        if constexpr (!BACK)
+#pragma unroll
+            for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < R; ++p) {
+                        const int i = tile_of(ii);
+                        ym[ii][s][p] = load_frag(a.ym + (val * R + p) * kTri + low_frag(i, min(s, i / 2)) * kFrag, lane);
+                    }
     };
-
-    Next x;
-    if (P == 1 && chunks > 0) load(0, x);
+    if (chunks > 0) {
+        load_a(0);
+        load_v(0);
+        load_c(0);
+        load_d(0);
+    }
     for (int c = 0; c < chunks; ++c) {
-        if constexpr (P > 1) load(c, x);             // registers do not hold two chunks' operands
-        Next nx;
-        if (P == 1 && c + 1 < chunks) load(c + 1, nx);
-        const size_t val = (size_t)(base + c) * a.Hv + hv;
+        const size_t val = val_of(c);
+        const int next = min(c + 1, chunks - 1);
         // parts of K H and Q H
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
@@ -350,99 +398,104 @@ __global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
                     for (int r = 0; r < 4; ++r)
                         to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = h[t][cc][r];
             }
+            f32x4 x[4], y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                part[0][wv][i][cc][lane] = mma<P, S>(x.kf[i], hb, f32x4{0, 0, 0, 0});
-                if constexpr (!BACK) part[Y - 1][wv][i][cc][lane] = mma<P, R>(x.qf[i], hb, f32x4{0, 0, 0, 0});
+                x[i] = mma<P, S>(kf[i], hb, f32x4{0, 0, 0, 0});
+                if constexpr (!BACK) y[i] = mma<P, R>(qf[i], hb, f32x4{0, 0, 0, 0});
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                part[0][wv][i][cc][lane] = x[i];
+                if constexpr (!BACK) part[Y - 1][wv][i][cc][lane] = y[i];
             }
         }
+        load_a(next);
         lds_barrier();
         f32x4 qh[NI][NC], f[NI][NC];
+        if (work) {
 #pragma unroll
-        for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = tile_of(ii);
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                f32x4 s = part[0][0][i][cc][lane];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) s += part[0][w][i][cc][lane];
-                f[ii][cc] = x.v[ii][cc] - x.ca[ii] * s;
-                put4<S>(&rr[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, x.cb[ii] * f[ii][cc]);
-                if constexpr (!BACK) {
-                    s = part[Y - 1][0][i][cc][lane];
-#pragma unroll
-                    for (int w = 1; w < NW; ++w) s += part[Y - 1][w][i][cc][lane];
-                    qh[ii][cc] = x.ca[ii] * s;
+                for (int cc = 0; cc < NC; ++cc) {
+                    const f32x4 kh = gather<NW>(&part[0][0][i][cc][lane], 4 * NC * 64);
+                    if constexpr (!BACK) qh[ii][cc] = ca[ii] * gather<NW>(&part[Y - 1][0][i][cc][lane], 4 * NC * 64);
+                    f[ii][cc] = v[ii][cc].get(seq.n, c * kC + 16 * i + 4 * q4, col0 + 16 * cc, a.dv) - ca[ii] * kh;
+                    put4<S>(&rr[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * f[ii][cc]);
                 }
             }
         }
+        load_v(next);
         lds_barrier();
         // W = F - M R, U = beta W
+        if (work) {
 #pragma unroll
-        for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = tile_of(ii);
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                f32x4 m = {0, 0, 0, 0};
+                for (int cc = 0; cc < NC; ++cc) {
+                    f32x4 m = {0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s > i / 2) continue;
-                    bf16x8 r[S];
-                    get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, r);
-                    m = mma<S, S>(x.tm[ii][s], r, m);
-                }
-                const f32x4 w = f[ii][cc] - m, u = x.cb[ii] * w;
-                put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, x.ce[ii] * u);
-                if constexpr (BACK) {
-                    float* to = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
+                    for (int s = 0; s < 2; ++s) {
+                        if (s > i / 2) continue;
+                        bf16x8 r[S];
+                        get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], kPl, r);
+                        m = mma<S, S>(tm[ii][s], r, m);
+                    }
+                    const f32x4 w = f[ii][cc] - m, u = cb[ii] * w;
+                    put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], kPl, ce[ii] * u);
+                    if constexpr (BACK) {
+                        float* to = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) to[(size_t)r * a.dvp] = w[r];
-                } else {
-                    put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], NC * 16 * kTp, u);
+                        for (int r = 0; r < 4; ++r) to[(size_t)r * a.dvp] = w[r];
+                    } else {
+                        put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], kPl, u);
+                    }
                 }
             }
         }
+        load_c(next);
         lds_barrier();
         // H' and the outputs
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
             bf16x8 u[2][S];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) get8<S>(&ue[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, u[s]);
+            for (int s = 0; s < 2; ++s) get8<S>(&ue[0][16 * cc + n][32 * s + 8 * q4], kPl, u[s]);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                h[t][cc] = x.end * h[t][cc];
+                h[t][cc] = end * h[t][cc];
 #pragma unroll
-                for (int s = 0; s < 2; ++s) h[t][cc] = mma<P, S>(x.kt[t][s], u[s], h[t][cc]);
+                for (int s = 0; s < 2; ++s) h[t][cc] = mma<P, S>(kt[t][s], u[s], h[t][cc]);
             }
         }
         if constexpr (!BACK) {
+            if (work) {
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = wv + ii * NW;
-                if (i >= 4) break;
+                for (int ii = 0; ii < NI; ++ii) {
+                    const int i = tile_of(ii);
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    f32x4 o = qh[ii][cc];
+                    for (int cc = 0; cc < NC; ++cc) {
+                        f32x4 o = qh[ii][cc];
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (s > i / 2) continue;
-                        bf16x8 u[R];
-                        get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], NC * 16 * kTp, u);
-                        o = mma<R, R>(x.ym[ii][s], u, o);
-                    }
+                        for (int s = 0; s < 2; ++s) {
+                            if (s > i / 2) continue;
+                            bf16x8 u[R];
+                            get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                            o = mma<R, R>(ym[ii][s], u, o);
+                        }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
-                        if (row < seq.n && col < a.dv)
-                            st_io<IO>(a.o.p, (size_t)((seq.row0 + row) * a.o.row + hv * a.o.head + col), o[r]);
+                        for (int r = 0; r < 4; ++r) {
+                            const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
+                            if (row < seq.n && col < a.dv)
+                                st_io<IO>(a.o.p, (size_t)((seq.row0 + row) * a.o.row + hv * a.o.head + col), o[r]);
+                        }
                     }
                 }
             }
         }
-        if (P == 1 && c + 1 < chunks) x = nx;
+        load_d(next);
     }
     if (!BACK && a.S_out) {
 #pragma unroll
@@ -495,10 +548,12 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
     const int slices = a.dvp / (16 * NC);
     scan_place<IO, DK>(a, slices, b, hv, sl);
     const int hk = hv / a.group;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
     const RuleSeq seq = rule_seq(a, b);
     const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
     const int col0 = sl * 16 * NC + n;
+    const bool work = NW <= 4 || wv < 4;
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
 
@@ -514,79 +569,97 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
                 dh[t][c][r] = a.dS_out && i < a.dk && j < a.dv ? a.dS_out[state + (size_t)j * a.dk + i] : 0.f;
             }
 
-    struct Next {
-        bf16x8 kf[4][P], kt[2][2][P], qt[2][2][P], tt[NI][2][S], yt[NI][2][S];
-        f32x4 ca[NI], ce[NI], cb[NI], d_o[NI][NC], w[NI][NC], h[2][NC];
-        float end;
-    };
-    auto load = [&](int c, Next& x) {
-        const size_t key = ((size_t)(base + c) * a.Hk + hk) * kTile, val = (size_t)(base + c) * a.Hv + hv;
-        const float* co = a.coef + val * 3 * kC;
+    // requested for the chunk before as soon as they have been used, as in rule_scan
+    bf16x8 kf[4][P], kt[2][2][P], qt[2][2][P], tt[NI][2][S], yt[NI][2][S];
+    f32x4 ca[NI], ce[NI], cb[NI], w[NI][NC], h[2][NC];
+    Raw4<IO> raw[NI][NC];
+    float end;
+    auto tile_of = [&](int ii) { return NW <= 4 ? wv + ii * NW : min(wv, 3); };
+    auto key_of = [&](int c) { return ((size_t)(base + c) * a.Hk + hk) * kTile; };
+    auto val_of = [&](int c) { return (size_t)(base + c) * a.Hv + hv; };
+    auto load_a = [&](int c) {
+        const size_t key = key_of(c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int p = 0; p < P; ++p) x.kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+            for (int p = 0; p < P; ++p) kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
+        const float* from = a.ht + (val_of(c) * DK + 32 * wv + 4 * q4) * a.dvp + col0;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) h[t][cc][r] = from[(size_t)(16 * t + r) * a.dvp + 16 * cc];
+        end = a.coef[val_of(c) * 3 * kC + kC - 1];
+    };
+    auto load_b = [&](int c) {
+        const size_t val = val_of(c);
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
-            x.ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
-            x.ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
-            x.cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+            const int i = tile_of(ii);
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                if (s < i / 2) continue;
+            for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int p = 0; p < S; ++p) {
-                    x.tt[ii][s][p] = load_frag(a.tt + (val * S + p) * kTri + up_frag(i, s) * kFrag, lane);
-                    x.yt[ii][s][p] = load_frag(a.yt + (val * S + p) * kTri + up_frag(i, s) * kFrag, lane);
-                }
-            }
-            const float* w = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0;
+                for (int p = 0; p < S; ++p)
+                    yt[ii][s][p] = load_frag(a.yt + (val * S + p) * kTri + up_frag(i, max(s, i / 2)) * kFrag, lane);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = c * kC + 16 * i + 4 * q4 + r;
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    const int col = col0 + 16 * cc;
-                    const bool in = row < seq.n && col < a.dv;
-                    x.d_o[ii][cc][r] =
-                        in ? ld_io<IO>(a.d_o.p, (size_t)((seq.row0 + row) * a.d_o.row + hv * a.d_o.head + col)) : 0.f;
-                    x.w[ii][cc][r] = w[(size_t)r * a.dvp + 16 * cc];
-                }
-            }
+            for (int cc = 0; cc < NC; ++cc)
+                raw[ii][cc].load(a.d_o, seq.row0, seq.n, c * kC + 16 * i + 4 * q4, hv * a.d_o.head, col0 + 16 * cc, a.dv);
         }
-        const float* h = a.ht + (val * DK + 32 * wv + 4 * q4) * a.dvp + col0;
+    };
+    auto load_c = [&](int c) {
+        const size_t val = val_of(c);
+        const float* co = a.coef + val * 3 * kC;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = tile_of(ii);
+            ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
+            ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
+            cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < S; ++p)
+                    tt[ii][s][p] = load_frag(a.tt + (val * S + p) * kTri + up_frag(i, max(s, i / 2)) * kFrag, lane);
+            const float* from = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0;
+#pragma unroll
+            for (int cc = 0; cc < NC; ++cc)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[ii][cc][r] = from[(size_t)r * a.dvp + 16 * cc];
+        }
+    };
+    auto load_d = [&](int c) {
+        const size_t key = key_of(c);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < P; ++p) {
-                    x.kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
-                    x.qt[t][s][p] = load_frag(a.qt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+                    kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
+                    qt[t][s][p] = load_frag(a.qt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
                 }
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) x.h[t][cc][r] = h[(size_t)(16 * t + r) * a.dvp + 16 * cc];
-        }
-        x.end = co[kC - 1];
     };
-
-    Next x;
-    if (P == 1 && chunks > 0) load(chunks - 1, x);
+    if (chunks > 0) {
+        load_b(chunks - 1);
+        load_a(chunks - 1);
+        load_c(chunks - 1);
+        load_d(chunks - 1);
+    }
     for (int c = chunks - 1; c >= 0; --c) {
-        if constexpr (P > 1) load(c, x);
-        Next nx;
-        if (P == 1 && c > 0) load(c - 1, nx);
-        const size_t val = (size_t)(base + c) * a.Hv + hv;
+        const size_t val = val_of(c);
+        const int next = max(c - 1, 0);
+        f32x4 d_o[NI][NC];
+        if (work) {
 #pragma unroll
-        for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = tile_of(ii);
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc) put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, x.d_o[ii][cc]);
+                for (int cc = 0; cc < NC; ++cc) {
+                    d_o[ii][cc] = raw[ii][cc].get(seq.n, c * kC + 16 * i + 4 * q4, col0 + 16 * cc, a.dv);
+                    put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, d_o[ii][cc]);
+                }
+            }
         }
         // parts of K dH', and a_C <H, dH'>
         float pa = 0.f;
@@ -604,75 +677,82 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = dh[t][cc][r];
-                    pa += x.h[t][cc][r] * dh[t][cc][r];
+                    pa += h[t][cc][r] * dh[t][cc][r];
                 }
+            f32x4 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) part[wv][i][cc][lane] = mma<P, S>(x.kf[i], hb, f32x4{0, 0, 0, 0});
+            for (int i = 0; i < 4; ++i) x[i] = mma<P, S>(kf[i], hb, f32x4{0, 0, 0, 0});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[wv][i][cc][lane] = x[i];
         }
-        pa = row_sum(x.end * pa);
+        const float decay = end;
+        pa = row_sum(decay * pa);
         if (n == 0) a.pa[((val * slices + sl) * NW + wv) * 4 + q4] = pa;
+        load_a(next);
         lds_barrier();
         f32x4 du[NI][NC], pe[NI];
+        if (work) {
 #pragma unroll
-        for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = tile_of(ii);
+                pe[ii] = f32x4{0, 0, 0, 0};
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                f32x4 s = part[0][i][cc][lane];
+                for (int cc = 0; cc < NC; ++cc) {
+                    f32x4 s = ce[ii] * gather<NW>(&part[0][i][cc][lane], 4 * NC * 64);
+                    pe[ii] += s * cb[ii] * w[ii][cc];
 #pragma unroll
-                for (int w = 1; w < NW; ++w) s += part[w][i][cc][lane];
-                s *= x.ce[ii];
-                pe[ii] = (cc ? pe[ii] : f32x4{0, 0, 0, 0}) + s * x.cb[ii] * x.w[ii][cc];
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    if (st < i / 2) continue;
-                    bf16x8 d[P];
-                    get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
-                    s = mma<S, P>(x.yt[ii][st], d, s);
+                    for (int st = 0; st < 2; ++st) {
+                        if (st < i / 2) continue;
+                        bf16x8 d[P];
+                        get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
+                        s = mma<S, P>(yt[ii][st], d, s);
+                    }
+                    du[ii][cc] = s;
+                    put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * s);
+                    put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, ca[ii] * d_o[ii][cc]);
                 }
-                du[ii][cc] = s;
-                put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, x.cb[ii] * s);
-                put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, x.ca[ii] * x.d_o[ii][cc]);
             }
         }
+        load_b(next);
         lds_barrier();
         // dR = dU - M^T beta dU
+        if (work) {
 #pragma unroll
-        for (int ii = 0; ii < NI; ++ii) {
-            const int i = wv + ii * NW;
-            if (i >= 4) break;
-            f32x4 pb = {0, 0, 0, 0};
+            for (int ii = 0; ii < NI; ++ii) {
+                const int i = tile_of(ii);
+                f32x4 pb = {0, 0, 0, 0};
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc) {
-                f32x4 m = {0, 0, 0, 0};
+                for (int cc = 0; cc < NC; ++cc) {
+                    f32x4 m = {0, 0, 0, 0};
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (s < i / 2) continue;
-                    bf16x8 u[S];
-                    get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
-                    m = mma<S, S>(x.tt[ii][s], u, m);
+                    for (int s = 0; s < 2; ++s) {
+                        if (s < i / 2) continue;
+                        bf16x8 u[S];
+                        get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                        m = mma<S, S>(tt[ii][s], u, m);
+                    }
+                    const f32x4 dr = du[ii][cc] - m, dv = cb[ii] * dr;
+                    put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -ca[ii] * dv);
+                    float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
+                        to[(size_t)r * a.dvp] = dr[r];
+                        if (row < seq.n && col < a.dv)
+                            st_io<IO>(a.dv_out.p, (size_t)((seq.row0 + row) * a.dv_out.row + hv * a.dv_out.head + col), dv[r]);
+                    }
+                    pb += dr * w[ii][cc];
                 }
-                const f32x4 dr = du[ii][cc] - m, dv = x.cb[ii] * dr;
-                put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -x.ca[ii] * dv);
-                float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
-                    to[(size_t)r * a.dvp] = dr[r];
-                    if (row < seq.n && col < a.dv)
-                        st_io<IO>(a.dv_out.p, (size_t)((seq.row0 + row) * a.dv_out.row + hv * a.dv_out.head + col), dv[r]);
+                for (int r = 0; r < 4; ++r) pb[r] = row_sum(pb[r]), pe[ii][r] = row_sum(pe[ii][r]);
+                if (n == 0) {
+                    const size_t at = (val * slices + sl) * kC + 16 * i + 4 * q4;
+                    *reinterpret_cast<f32x4*>(a.pb + at) = pb;
+                    *reinterpret_cast<f32x4*>(a.pe + at) = pe[ii];
                 }
-                pb += dr * x.w[ii][cc];
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) pb[r] = row_sum(pb[r]), pe[ii][r] = row_sum(pe[ii][r]);
-            if (n == 0) {
-                const size_t at = (val * slices + sl) * kC + 16 * i + 4 * q4;
-                *reinterpret_cast<f32x4*>(a.pb + at) = pb;
-                *reinterpret_cast<f32x4*>(a.pe + at) = pe[ii];
             }
         }
+        load_c(next);
         lds_barrier();
         // dH
 #pragma unroll
@@ -685,15 +765,15 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                dh[t][cc] = x.end * dh[t][cc];
+                dh[t][cc] = decay * dh[t][cc];
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-                    dh[t][cc] = mma<P, S>(x.qt[t][s], u[s], dh[t][cc]);
-                    dh[t][cc] = mma<P, S>(x.kt[t][s], z[s], dh[t][cc]);
+                    dh[t][cc] = mma<P, S>(qt[t][s], u[s], dh[t][cc]);
+                    dh[t][cc] = mma<P, S>(kt[t][s], z[s], dh[t][cc]);
                 }
             }
         }
-        if (P == 1 && c > 0) x = nx;
+        load_d(next);
     }
     if (a.dS0) {
 #pragma unroll
@@ -744,7 +824,8 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int slices
     const int slot = blockIdx.x, hk = blockIdx.y;
     const RuleChunk ch = rule_chunk(a, slot);
     if (ch.n == 0) return;
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, n = lane & 15, q4 = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
     const size_t key = ((size_t)slot * a.Hk + hk) * kTile;
     const int col = 16 * wv + n;
 
