@@ -111,8 +111,9 @@ __host__ __device__ constexpr int up_frag(int i, int s) { return i < 2 ? 2 * i +
 constexpr int kTriFrags = 6;
 constexpr int kFrag = 64 * 16;               // bytes of one fragment: 16 per lane
 
+// p the same for the wave: the lane's part of the address is a 32-bit offset of its own.
 __device__ __forceinline__ bf16x8 load_frag(const char* p, int lane) {
-    return *reinterpret_cast<const bf16x8*>(p + lane * 16);
+    return *reinterpret_cast<const bf16x8*>(p + (uint32_t)(lane * 16));
 }
 __device__ __forceinline__ void store_frag(char* p, int lane, bf16x8 x) {
     *reinterpret_cast<bf16x8*>(p + lane * 16) = x;
@@ -128,26 +129,50 @@ constexpr int kSum = 3;                              // an fp32 factor
 template <int IO>
 constexpr int kRound = IO == GDN_BF16 ? 2 : 3;       // an fp32 factor of a product for io rows alone
 
+// Two values as the next term of each, packed; what is left of them stays in x and y.
+__device__ __forceinline__ uint32_t next_term(float& x, float& y, bool last) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const uint32_t t = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
+    if (!last) {
+        x -= __uint_as_float(t << 16);
+        y -= __uint_as_float(t & 0xffff0000u);
+    }
+    return t;
+}
 template <int P>
 __device__ __forceinline__ void split8(const float (&x)[8], bf16x8 (&to)[P]) {
+    u32x4 t[P];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        float rest = x[j];
+    for (int j = 0; j < 4; ++j) {
+        float u = x[2 * j], v = x[2 * j + 1];
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            to[p][j] = (__bf16)rest;
-            rest -= (float)to[p][j];
-        }
+        for (int p = 0; p < P; ++p) t[p][j] = next_term(u, v, p == P - 1);
     }
+#pragma unroll
+    for (int p = 0; p < P; ++p) to[p] = __builtin_bit_cast(bf16x8, t[p]);
 }
 template <int P>
 __device__ __forceinline__ void split4p(f32x4 x, s16x4 (&to)[P]) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 t[P];
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const bf16x4 h = __builtin_convertvector(x, bf16x4);
-        to[p] = __builtin_bit_cast(s16x4, h);
-        x -= __builtin_convertvector(h, f32x4);
+    for (int j = 0; j < 2; ++j) {
+        float u = x[2 * j], v = x[2 * j + 1];
+#pragma unroll
+        for (int p = 0; p < P; ++p) t[p][j] = next_term(u, v, p == P - 1);
     }
+#pragma unroll
+    for (int p = 0; p < P; ++p) to[p] = __builtin_bit_cast(s16x4, t[p]);
+}
+
+// An io element, rounded to nearest.
+template <int IO>
+__device__ __forceinline__ void put_io(char* p, int64_t i, float x) {
+    if constexpr (IO == GDN_BF16)
+        reinterpret_cast<uint16_t*>(p)[i] = bf16_rne(x);
+    else
+        reinterpret_cast<float*>(p)[i] = x;
 }
 
 template <int IO>

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
         bf16x8 x[decltype(planes)::value];
         split8(v, x);
 #pragma unroll
-        for (int p = 0; p < decltype(planes)::value; ++p) store_frag(to + (p * kTriFrags + f) * kFrag, lane, x[p]);
+        for (int p = 0; p < decltype(planes)::value; ++p) store_frag(to + (f * decltype(planes)::value + p) * kFrag, lane, x[p]);
     };
     auto low = [&](const float (*x)[TP], char* to, auto planes) {
         for (int f = wv; f < kTriFrags; f += 4) {
@@ -217,11 +217,19 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
 
 // ------------------------------------------------------------------ scan
 //
-// One workgroup per (sequence, value head, slice of 16 NC value columns), d_k / 32 waves.  Wave w
-// keeps rows 32 w .. 32 w + 31 of the slice of H in accumulators (fp32), which are one contraction
-// step of K H and Q H: each wave forms its part of those products from registers alone, the parts
-// meet in LDS, and then row tile i of the chunk (16 rows) is worked on by wave i.  Operands of a
-// chunk are requested while the chunk before it is worked on.
+// One workgroup per (sequence, value head, slice of 16 NC value columns).  d_k / 32 state waves:
+// wave w keeps rows 32 w .. 32 w + 31 of the slice of H in accumulators (fp32).  A chunk goes in four
+// phases with a barrier between them: every wave's H goes to LDS as operand terms; row tile i (16
+// rows) of K H, then of W, is formed by wave i, which needs all of the one before; H' needs all of
+// U.  The outputs are formed by waves of their own, from the terms of H and U that the state waves
+// leave in LDS, in the time that those take for the next step.  Terms lie in LDS as
+// [column][row], where accumulators have four rows to a lane (8-byte writes) and operands eight
+// (16-byte reads).  (Parts of K H from each wave's own rows of H, added up in LDS, took 1.1 times as
+// long: 16-byte LDS writes take 20 to 40 cycles each where reads take 9.)
+//
+// A single sequence's scan is bound by what one state wave issues per chunk, one after the other,
+// so addresses are kept as running pointers, and operands of a chunk are requested while the chunk
+// before it is worked on.
 // BACK: instead of the outputs, the state before each chunk and W are kept for the gradients.
 template <int IO, int DK>
 __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b, int& hv, int& sl) {
@@ -240,62 +248,194 @@ __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b
     hv = head - b * a.Hv;
 }
 
-// Elements of a value row, four rows of one column, as they lie in memory: requested a chunk ahead,
-// converted and masked where they are used, so that nothing waits for them before.
+// Elements of value rows, four rows 16 i + 4 q4 + r of a chunk in one column: requested a chunk
+// ahead as they lie in memory, converted and masked where they are used, so that nothing waits for
+// them before.  A lane's four places are kept as offsets from the chunk's first row; the last
+// chunk's rows past the sequence's end are read from its last row.
 template <int IO>
-struct Raw4 {
+struct Rows4 {
     typedef std::conditional_t<IO == GDN_BF16, uint16_t, float> E;
+    const E* at;                                     // column of the chunk's first row
+    int64_t step;                                    // a chunk's rows
+    int64_t off[4];
     E x[4];
-    __device__ __forceinline__ void load(const Rows& from, int64_t row0, int rows, int row, int64_t head, int col, int d) {
-        const E* p = reinterpret_cast<const E*>(from.p) + head + min(col, d - 1);
+    int row;                                         // of the chunk
+    bool in;                                         // a column of the tensor
+    __device__ __forceinline__ void begin(const Rows& from, int64_t row0, int64_t head, int row_, int col, int d) {
+        at = reinterpret_cast<const E*>(from.p) + row0 * from.row + head + min(col, d - 1);
+        step = kC * from.row;
+        row = row_;
+        in = col < d;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = p[(row0 + min(row + r, rows - 1)) * from.row];
+        for (int r = 0; r < 4; ++r) off[r] = (row + r) * from.row;
     }
-    __device__ __forceinline__ f32x4 get(int rows, int row, int col, int d) const {
+    // the places of a chunk of `rows` rows, fewer than kC
+    __device__ __forceinline__ void last(int64_t stride, int rows) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) off[r] = min(row + r, rows - 1) * stride;
+    }
+    __device__ __forceinline__ void load(int64_t chunk) {
+        const E* p = at + chunk * step;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = p[off[r]];
+    }
+    __device__ __forceinline__ f32x4 get(int rows) const {
         f32x4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             float y;
             if constexpr (IO == GDN_BF16) y = bf16_bits_to_f32(x[r]); else y = x[r];
-            v[r] = row + r < rows && col < d ? y : 0.f;
+            v[r] = in && row + r < rows ? y : 0.f;
         }
         return v;
     }
 };
 
-// Parts of a product from the waves of a workgroup, as one.
-template <int NW>
-__device__ __forceinline__ f32x4 gather(const f32x4* part, int stride) {
-    f32x4 t[NW];
-#pragma unroll
-    for (int w = 0; w < NW; ++w) t[w] = part[w * stride];
-#pragma unroll
-    for (int w = 1; w < NW; ++w) t[0] += t[w];
-    return t[0];
-}
+// Which row tiles and columns of a slice a wave works on: items x < kItems of the wave's row tiles
+// ii < NI.  With eight waves the two halves take one column block each.
+template <int NW, int NC>
+struct Deal {
+    static_assert(NW <= 4 || NC == 2, "eight waves share two column blocks");
+    static constexpr int NI = NW < 4 ? 4 / NW : 1;
+    static constexpr int NX = NW <= 4 ? NC : 1;      // column blocks of a wave
+    int wv;
+    __device__ int tile(int ii) const { return NW <= 4 ? wv + ii * NW : wv & 3; }
+    __device__ int block(int x) const { return NW <= 4 ? x : wv >> 2; }
+};
+
+// Waves of the outputs.
+template <int DK>
+constexpr int kOutWaves = DK / 32 < 4 ? DK / 32 : 4;
 
 template <int IO, int DK, int NC, bool BACK>
-__global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
+__global__ void __launch_bounds__(DK * 2 + (BACK ? 0 : 64 * kOutWaves<DK>), IO == GDN_BF16 && DK <= 128 ? 2 : 1)
+rule_scan(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
-    constexpr int NI = NW < 4 ? 4 / NW : 1;          // row tiles of a wave (waves past the fourth have none)
     constexpr int S = kSum, R = kRound<IO>;
-    constexpr int Y = BACK ? 1 : 2;                  // products that meet in LDS: K H, and Q H
-    constexpr int kPl = NC * 16 * kTp;               // elements of a plane of a [column][row] tile
-    __shared__ f32x4 part[Y][NW][4][NC][64];
-    __shared__ __attribute__((aligned(16))) uint16_t rr[S][NC * 16][kTp], uu[R][NC * 16][kTp], ue[S][NC * 16][kTp];
+    typedef Deal<NW, NC> D;
+    constexpr int NI = D::NI, NX = D::NX;
+    constexpr bool kHold = DK * P <= 256;            // K and Q are held in registers, or read as they are used
+    constexpr int KH = kHold ? KS : 1;
+    constexpr int LH = DK + 8;
+    constexpr int kPl = NC * 16 * kTp, kPh = NC * 16 * LH; // elements of a plane of a [column][row] tile
+    __shared__ __attribute__((aligned(16))) uint16_t hh[S][NC * 16][LH], rr[S][NC * 16][kTp], uu[R][NC * 16][kTp],
+        ue[S][NC * 16][kTp];
 
     int b, hv, sl;
     scan_place<IO, DK>(a, a.dvp / (16 * NC), b, hv, sl);
     const int hk = hv / a.group;
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q4 = lane >> 4;
-    const bool work = NW <= 4 || wv < 4;
     const RuleSeq seq = rule_seq(a, b);
     const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
+    const int tail = seq.n - (chunks - 1) * kC;      // rows of the last chunk
     const int col0 = sl * 16 * NC + n;               // this lane's columns: col0 + 16 c
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
+    const size_t key = ((size_t)base * a.Hk + hk) * kTile, val = (size_t)base * a.Hv + hv;
+    const size_t key_step = (size_t)a.Hk * kTile;
+    const float* co = a.coef + val * 3 * kC;         // of the chunk that is worked on
+    const size_t co_step = (size_t)a.Hv * 3 * kC;
 
+    if (!BACK && wv >= NW) {
+        // ---- the outputs: O = a Q H + Y U
+        constexpr int OW = kOutWaves<DK>, OI = 4 / OW;
+        const int first = wv - NW;
+        bf16x8 qf[OI][KH][P], ym[OI][2][R];
+        f32x4 ca[OI];
+        const char* pq = a.qf + key;
+        const char* py = a.ym + val * R * kTri;
+        const float* pc = co;
+        const size_t y_step = (size_t)a.Hv * R * kTri;
+        auto load_q = [&](const char* at, int s, int to) {
+#pragma unroll
+            for (int ii = 0; ii < OI; ++ii)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    qf[ii][to][p] = load_frag(at + ((p * 4 + first + ii * OW) * KS + s) * kFrag, lane);
+        };
+        auto load = [&](bool on) {
+            if constexpr (kHold)
+#pragma unroll
+                for (int s = 0; s < KS; ++s) load_q(pq, s, s);
+            (void)on;
+        };
+        auto load_y = [&] {
+#pragma unroll
+            for (int ii = 0; ii < OI; ++ii) {
+                const int i = first + ii * OW;
+                ca[ii] = *reinterpret_cast<const f32x4*>(pc + 16 * i + 4 * q4);
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < R; ++p)
+                        ym[ii][s][p] = load_frag(py + (low_frag(i, min(s, i / 2)) * R + p) * kFrag, lane);
+            }
+        };
+        int64_t off[OI][4];                          // this lane's rows of a chunk of o
+#pragma unroll
+        for (int ii = 0; ii < OI; ++ii)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) off[ii][r] = (16 * (first + ii * OW) + 4 * q4 + r) * a.o.row;
+        if (chunks > 0) {
+            load(true);
+            load_y();
+        }
+        for (int c = 0; c < chunks; ++c) {
+            const bool more = c + 1 < chunks;
+            const char* pq_now = pq;
+            f32x4 o[OI][NC];
+#pragma unroll
+            for (int ii = 0; ii < OI; ++ii)
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) o[ii][cc] = f32x4{0, 0, 0, 0};
+            lds_barrier();
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                if constexpr (!kHold) load_q(pq_now, s, 0);
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) {
+                    bf16x8 hb[R];
+                    get8<R>(&hh[0][16 * cc + n][32 * s + 8 * q4], kPh, hb);
+#pragma unroll
+                    for (int ii = 0; ii < OI; ++ii) o[ii][cc] = mma<P, R>(qf[ii][kHold ? s : 0], hb, o[ii][cc]);
+                }
+            }
+            pq += more ? key_step : 0;
+            load(more);
+            lds_barrier();
+            lds_barrier();
+            const int rows = more ? kC : tail;
+            char* to = a.o.p + ((seq.row0 + (int64_t)c * kC) * a.o.row + hv * a.o.head) * (IO == GDN_BF16 ? 2 : 4);
+#pragma unroll
+            for (int ii = 0; ii < OI; ++ii) {
+                const int i = first + ii * OW;
+#pragma unroll
+                for (int cc = 0; cc < NC; ++cc) {
+                    f32x4 x = ca[ii] * o[ii][cc];
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (s > i / 2) continue;
+                        bf16x8 u[R];
+                        get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                        x = mma<R, R>(ym[ii][s], u, x);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * i + 4 * q4 + r < rows && col0 + 16 * cc < a.dv)
+                            put_io<IO>(to, off[ii][r] + col0 + 16 * cc, x[r]);
+                }
+            }
+            py += more ? y_step : 0;
+            pc += more ? co_step : 0;
+            load_y();
+        }
+        return;
+    }
+
+    // ---- the state
+    const D deal{wv};
+    __builtin_amdgcn_s_setprio(2);                   // the outputs' waves fill in
     // H: rows 32 wv + 16 t + 4 q4 + r, columns col0 + 16 c
     f32x4 h[2][NC];
     const size_t state = ((size_t)b * a.Hv + hv) * a.dv * a.dk;
@@ -311,153 +451,143 @@ __global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
 
     // The operands of a chunk are requested for the next one as soon as they have been used.  No
     // request is conditional: the compiler could not count the ones in flight, and would wait for all.
-    bf16x8 kf[4][P], qf[BACK ? 1 : 4][P], tm[NI][2][S], ym[BACK ? 1 : NI][2][R], kt[2][2][P];
+    bf16x8 kf[NI][KH][P], tm[NI][2][S], kt[2][2][P];
     f32x4 ca[NI], ce[NI], cb[NI];
-    Raw4<IO> v[NI][NC];
+    Rows4<IO> v[NI][NX];
     float end;
-    auto tile_of = [&](int ii) { return NW <= 4 ? wv + ii * NW : min(wv, 3); };
-    auto key_of = [&](int c) { return ((size_t)(base + c) * a.Hk + hk) * kTile; };
-    auto val_of = [&](int c) { return (size_t)(base + c) * a.Hv + hv; };
-    auto load_a = [&](int c) {
-        const size_t key = key_of(c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
-                if constexpr (!BACK) qf[i][p] = load_frag(a.qf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
-            }
-    };
-    auto load_v = [&](int c) {
+    const char* pk = a.kf + key;
+    const char* pt = a.kt + key + 2 * wv * 2 * kFrag;
+    const char* pm = a.tm + val * S * kTri;
+    const size_t m_step = (size_t)a.Hv * S * kTri;
+    const float *pca = co, *pcb = co;
+    float* ph = BACK ? a.ht + (val * DK + 32 * wv + 4 * q4) * a.dvp + col0 : nullptr;
+    float* pw = BACK ? a.w + (val * kC + 4 * q4) * a.dvp + col0 : nullptr;
+    auto load_k = [&](const char* at, int s, int to) {
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-                v[ii][cc].load(a.v, seq.row0, seq.n, c * kC + 16 * tile_of(ii) + 4 * q4, hv * a.v.head, col0 + 16 * cc, a.dv);
+            for (int p = 0; p < P; ++p) kf[ii][to][p] = load_frag(at + ((p * 4 + deal.tile(ii)) * KS + s) * kFrag, lane);
     };
-    auto load_c = [&](int c) {
-        const size_t val = val_of(c);
-        const float* co = a.coef + val * 3 * kC;
+    auto load_b = [&](int c) {
+        if constexpr (kHold)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) load_k(pk, s, s);
+        const bool part = c == chunks - 1 && tail < kC;
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
-            const int i = tile_of(ii);
-            ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
-            ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
-            cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
+            ca[ii] = *reinterpret_cast<const f32x4*>(pca + 16 * deal.tile(ii) + 4 * q4);
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                if (part) v[ii][x].last(a.v.row, tail);
+                v[ii][x].load(c);
+            }
+        }
+    };
+    auto load_c = [&] {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = deal.tile(ii);
+            ce[ii] = *reinterpret_cast<const f32x4*>(pcb + kC + 16 * i + 4 * q4);
+            cb[ii] = *reinterpret_cast<const f32x4*>(pcb + 2 * kC + 16 * i + 4 * q4);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < S; ++p)
-                    tm[ii][s][p] = load_frag(a.tm + (val * S + p) * kTri + low_frag(i, min(s, i / 2)) * kFrag, lane);
+                    tm[ii][s][p] = load_frag(pm + (low_frag(i, min(s, i / 2)) * S + p) * kFrag, lane);
         }
     };
-    auto load_d = [&](int c) {
-        const size_t key = key_of(c), val = val_of(c);
+    auto load_d = [&] {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    kt[t][s][p] = load_frag(a.kt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
-        end = a.coef[val * 3 * kC + kC - 1];
-        if constexpr (!BACK)
-#pragma unroll
-            for (int ii = 0; ii < NI; ++ii)
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int p = 0; p < R; ++p) {
-                        const int i = tile_of(ii);
-                        ym[ii][s][p] = load_frag(a.ym + (val * R + p) * kTri + low_frag(i, min(s, i / 2)) * kFrag, lane);
-                    }
+                for (int p = 0; p < P; ++p) kt[t][s][p] = load_frag(pt + ((p * NT + t) * 2 + s) * kFrag, lane);
+        end = co[kC - 1];
     };
+#pragma unroll
+    for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+            v[ii][x].begin(a.v, seq.row0, hv * a.v.head, 16 * deal.tile(ii) + 4 * q4, col0 + 16 * deal.block(x), a.dv);
+    wait_vmem_all();                                 // for H, so that the loop's first wait is not for its operands too
     if (chunks > 0) {
-        load_a(0);
-        load_v(0);
-        load_c(0);
-        load_d(0);
+        load_b(0);
+        load_c();
+        load_d();
     }
     for (int c = 0; c < chunks; ++c) {
-        const size_t val = val_of(c);
-        const int next = min(c + 1, chunks - 1);
-        // parts of K H and Q H
+        const bool more = c + 1 < chunks;
+        const int rows = more ? kC : tail;
+        const char* pk_now = pk;
 #pragma unroll
-        for (int cc = 0; cc < NC; ++cc) {
-            bf16x8 hb[S];
-            s16x4 h0[S], h1[S];
-            split4p(h[0][cc], h0);
-            split4p(h[1][cc], h1);
+        for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-            for (int p = 0; p < S; ++p) hb[p] = stack_pair(h0[p], h1[p]);
-            if constexpr (BACK) {                    // the state before the chunk, for the gradients
-                float* to = a.ht + val * DK * a.dvp + col0 + 16 * cc;
+            for (int t = 0; t < 2; ++t) {
+                put4<S>(&hh[0][16 * cc + n][32 * wv + 16 * t + 4 * q4], kPh, h[t][cc]);
+                if constexpr (BACK)                  // the state before the chunk, for the gradients
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = h[t][cc][r];
+                    for (int r = 0; r < 4; ++r) ph[(16 * t + r) * a.dvp + 16 * cc] = h[t][cc][r];
             }
-            f32x4 x[4], y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = mma<P, S>(kf[i], hb, f32x4{0, 0, 0, 0});
-                if constexpr (!BACK) y[i] = mma<P, R>(qf[i], hb, f32x4{0, 0, 0, 0});
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                part[0][wv][i][cc][lane] = x[i];
-                if constexpr (!BACK) part[Y - 1][wv][i][cc][lane] = y[i];
-            }
-        }
-        load_a(next);
         lds_barrier();
-        f32x4 qh[NI][NC], f[NI][NC];
-        if (work) {
+        // F = V - a K H
+        f32x4 f[NI][NX];
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = tile_of(ii);
+        for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    const f32x4 kh = gather<NW>(&part[0][0][i][cc][lane], 4 * NC * 64);
-                    if constexpr (!BACK) qh[ii][cc] = ca[ii] * gather<NW>(&part[Y - 1][0][i][cc][lane], 4 * NC * 64);
-                    f[ii][cc] = v[ii][cc].get(seq.n, c * kC + 16 * i + 4 * q4, col0 + 16 * cc, a.dv) - ca[ii] * kh;
-                    put4<S>(&rr[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * f[ii][cc]);
-                }
+            for (int x = 0; x < NX; ++x) f[ii][x] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            if constexpr (!kHold) load_k(pk_now, s, 0);
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                bf16x8 hb[S];
+                get8<S>(&hh[0][16 * deal.block(x) + n][32 * s + 8 * q4], kPh, hb);
+#pragma unroll
+                for (int ii = 0; ii < NI; ++ii) f[ii][x] = mma<P, S>(kf[ii][kHold ? s : 0], hb, f[ii][x]);
             }
         }
-        load_v(next);
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                f[ii][x] = v[ii][x].get(rows) - ca[ii] * f[ii][x];
+                put4<S>(&rr[0][16 * deal.block(x) + n][16 * deal.tile(ii) + 4 * q4], kPl, cb[ii] * f[ii][x]);
+            }
+        pk += more ? key_step : 0;
+        pca += more ? co_step : 0;
+        load_b(more ? c + 1 : c);
         lds_barrier();
         // W = F - M R, U = beta W
-        if (work) {
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = tile_of(ii);
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = deal.tile(ii);
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    f32x4 m = {0, 0, 0, 0};
+            for (int x = 0; x < NX; ++x) {
+                const int cc = deal.block(x);
+                f32x4 m = {0, 0, 0, 0};
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (s > i / 2) continue;
-                        bf16x8 r[S];
-                        get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], kPl, r);
-                        m = mma<S, S>(tm[ii][s], r, m);
-                    }
-                    const f32x4 w = f[ii][cc] - m, u = cb[ii] * w;
-                    put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], kPl, ce[ii] * u);
-                    if constexpr (BACK) {
-                        float* to = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
+                for (int s = 0; s < 2; ++s) {
+                    if (s > i / 2) continue;
+                    bf16x8 r[S];
+                    get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], kPl, r);
+                    m = mma<S, S>(tm[ii][s], r, m);
+                }
+                const f32x4 w = f[ii][x] - m, u = cb[ii] * w;
+                put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], kPl, ce[ii] * u);
+                if constexpr (BACK) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) to[(size_t)r * a.dvp] = w[r];
-                    } else {
-                        put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], kPl, u);
-                    }
+                    for (int r = 0; r < 4; ++r) pw[(16 * i + r) * a.dvp + 16 * cc] = w[r];
+                } else {
+                    put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], kPl, u);
                 }
             }
         }
-        load_c(next);
+        pm += more ? m_step : 0;
+        pcb += more ? co_step : 0;
+        load_c();
         lds_barrier();
-        // H' and the outputs
+        // H'
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc) {
             bf16x8 u[2][S];
@@ -470,32 +600,13 @@ __global__ void __launch_bounds__(DK * 2) rule_scan(const RuleArgs a) {
                 for (int s = 0; s < 2; ++s) h[t][cc] = mma<P, S>(kt[t][s], u[s], h[t][cc]);
             }
         }
-        if constexpr (!BACK) {
-            if (work) {
-#pragma unroll
-                for (int ii = 0; ii < NI; ++ii) {
-                    const int i = tile_of(ii);
-#pragma unroll
-                    for (int cc = 0; cc < NC; ++cc) {
-                        f32x4 o = qh[ii][cc];
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            if (s > i / 2) continue;
-                            bf16x8 u[R];
-                            get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
-                            o = mma<R, R>(ym[ii][s], u, o);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
-                            if (row < seq.n && col < a.dv)
-                                st_io<IO>(a.o.p, (size_t)((seq.row0 + row) * a.o.row + hv * a.o.head + col), o[r]);
-                        }
-                    }
-                }
-            }
+        pt += more ? key_step : 0;
+        co += more ? co_step : 0;
+        load_d();
+        if constexpr (BACK) {
+            ph += (size_t)a.Hv * DK * a.dvp;
+            pw += (size_t)a.Hv * kC * a.dvp;
         }
-        load_d(next);
     }
     if (!BACK && a.S_out) {
 #pragma unroll
@@ -535,14 +646,16 @@ __device__ __forceinline__ float row_scan(float x) {
 // dbeta and of the terms of d ln g that reach the chunk's end: e^(Gamma_C - Gamma_j) k_j . dH' u_j
 // of every row, and a_C <H, dH'>.
 template <int IO, int DK, int NC>
-__global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
+__global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 ? 2 : 1) rule_scan_back(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
-    constexpr int NI = NW < 4 ? 4 / NW : 1;
     constexpr int S = kSum;
-    constexpr int kPl = NC * 16 * kTp;               // elements of a plane of a [column][row] tile
-    __shared__ f32x4 part[NW][4][NC][64];
-    __shared__ __attribute__((aligned(16))) uint16_t od[P][NC * 16][kTp], oa[S][NC * 16][kTp], ou[S][NC * 16][kTp],
-        oz[S][NC * 16][kTp];
+    typedef Deal<NW, NC> D;
+    constexpr int NI = D::NI, NX = D::NX;
+    constexpr bool kHold = DK * P <= 256;
+    constexpr int KH = kHold ? KS : 1, LH = DK + 8;
+    constexpr int kPl = NC * 16 * kTp, kPh = NC * 16 * LH; // elements of a plane of a [column][row] tile
+    __shared__ __attribute__((aligned(16))) uint16_t hh[S][NC * 16][LH], od[P][NC * 16][kTp], oa[S][NC * 16][kTp],
+        ou[S][NC * 16][kTp], oz[S][NC * 16][kTp];
 
     int b, hv, sl;
     const int slices = a.dvp / (16 * NC);
@@ -550,10 +663,10 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
     const int hk = hv / a.group;
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q4 = lane >> 4;
+    const D deal{wv};
     const RuleSeq seq = rule_seq(a, b);
     const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
     const int col0 = sl * 16 * NC + n;
-    const bool work = NW <= 4 || wv < 4;
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
 
@@ -570,19 +683,20 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
             }
 
     // requested for the chunk before as soon as they have been used, as in rule_scan
-    bf16x8 kf[4][P], kt[2][2][P], qt[2][2][P], tt[NI][2][S], yt[NI][2][S];
-    f32x4 ca[NI], ce[NI], cb[NI], w[NI][NC], h[2][NC];
-    Raw4<IO> raw[NI][NC];
+    bf16x8 kf[NI][KH][P], kt[2][2][P], qt[2][2][P], tt[NI][2][S], yt[NI][2][S];
+    f32x4 ca[NI], ce[NI], cb[NI], w[NI][NX], h[2][NC];
+    Rows4<IO> raw[NI][NX];
     float end;
-    auto tile_of = [&](int ii) { return NW <= 4 ? wv + ii * NW : min(wv, 3); };
     auto key_of = [&](int c) { return ((size_t)(base + c) * a.Hk + hk) * kTile; };
     auto val_of = [&](int c) { return (size_t)(base + c) * a.Hv + hv; };
+    auto load_k = [&](int c, int s, int to) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                kf[ii][to][p] = load_frag(a.kf + key_of(c) + ((p * 4 + deal.tile(ii)) * KS + s) * kFrag, lane);
+    };
     auto load_a = [&](int c) {
-        const size_t key = key_of(c);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p) kf[i][p] = load_frag(a.kf + key + ((p * 4 + i) * KS + wv) * kFrag, lane);
         const float* from = a.ht + (val_of(c) * DK + 32 * wv + 4 * q4) * a.dvp + col0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -591,20 +705,24 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) h[t][cc][r] = from[(size_t)(16 * t + r) * a.dvp + 16 * cc];
         end = a.coef[val_of(c) * 3 * kC + kC - 1];
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) raw[ii][x].load(c);
     };
     auto load_b = [&](int c) {
         const size_t val = val_of(c);
+        if constexpr (kHold)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) load_k(c, s, s);
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
-            const int i = tile_of(ii);
+            const int i = deal.tile(ii);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < S; ++p)
-                    yt[ii][s][p] = load_frag(a.yt + (val * S + p) * kTri + up_frag(i, max(s, i / 2)) * kFrag, lane);
-#pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
-                raw[ii][cc].load(a.d_o, seq.row0, seq.n, c * kC + 16 * i + 4 * q4, hv * a.d_o.head, col0 + 16 * cc, a.dv);
+                    yt[ii][s][p] = load_frag(a.yt + val * S * kTri + (up_frag(i, max(s, i / 2)) * S + p) * kFrag, lane);
         }
     };
     auto load_c = [&](int c) {
@@ -612,7 +730,7 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
         const float* co = a.coef + val * 3 * kC;
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
-            const int i = tile_of(ii);
+            const int i = deal.tile(ii);
             ca[ii] = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
             ce[ii] = *reinterpret_cast<const f32x4*>(co + kC + 16 * i + 4 * q4);
             cb[ii] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4);
@@ -620,12 +738,12 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int p = 0; p < S; ++p)
-                    tt[ii][s][p] = load_frag(a.tt + (val * S + p) * kTri + up_frag(i, max(s, i / 2)) * kFrag, lane);
+                    tt[ii][s][p] = load_frag(a.tt + val * S * kTri + (up_frag(i, max(s, i / 2)) * S + p) * kFrag, lane);
             const float* from = a.w + (val * kC + 16 * i + 4 * q4) * a.dvp + col0;
 #pragma unroll
-            for (int cc = 0; cc < NC; ++cc)
+            for (int x = 0; x < NX; ++x)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) w[ii][cc][r] = from[(size_t)r * a.dvp + 16 * cc];
+                for (int r = 0; r < 4; ++r) w[ii][x][r] = from[(size_t)r * a.dvp + 16 * deal.block(x)];
         }
     };
     auto load_d = [&](int c) {
@@ -640,116 +758,133 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
                     qt[t][s][p] = load_frag(a.qt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
                 }
     };
+    const int tail = seq.n - (chunks - 1) * kC;
+    auto places = [&](int rows) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) raw[ii][x].last(a.d_o.row, rows);
+    };
+#pragma unroll
+    for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+        for (int x = 0; x < NX; ++x)
+            raw[ii][x].begin(a.d_o, seq.row0, hv * a.d_o.head, 16 * deal.tile(ii) + 4 * q4, col0 + 16 * deal.block(x), a.dv);
+    wait_vmem_all();
     if (chunks > 0) {
-        load_b(chunks - 1);
+        places(tail);
         load_a(chunks - 1);
+        places(kC);
+        load_b(chunks - 1);
         load_c(chunks - 1);
         load_d(chunks - 1);
     }
     for (int c = chunks - 1; c >= 0; --c) {
         const size_t val = val_of(c);
         const int next = max(c - 1, 0);
-        f32x4 d_o[NI][NC];
-        if (work) {
+        // dH' and dO to LDS, and a_C <H, dH'>
+        f32x4 d_o[NI][NX];
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = tile_of(ii);
+        for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    d_o[ii][cc] = raw[ii][cc].get(seq.n, c * kC + 16 * i + 4 * q4, col0 + 16 * cc, a.dv);
-                    put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, d_o[ii][cc]);
-                }
+            for (int x = 0; x < NX; ++x) {
+                const int i = deal.tile(ii), cc = deal.block(x);
+                d_o[ii][x] = raw[ii][x].get(seq.n - c * kC);
+                put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, d_o[ii][x]);
             }
-        }
-        // parts of K dH', and a_C <H, dH'>
         float pa = 0.f;
 #pragma unroll
-        for (int cc = 0; cc < NC; ++cc) {
-            bf16x8 hb[S];
-            s16x4 h0[S], h1[S];
-            split4p(dh[0][cc], h0);
-            split4p(dh[1][cc], h1);
+        for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
-            for (int p = 0; p < S; ++p) hb[p] = stack_pair(h0[p], h1[p]);
-            float* to = a.dht + val * DK * a.dvp + col0 + 16 * cc;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 2; ++t) {
+                put4<S>(&hh[0][16 * cc + n][32 * wv + 16 * t + 4 * q4], kPh, dh[t][cc]);
+                float* to = a.dht + (val * DK + 32 * wv + 16 * t + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    to[(size_t)(32 * wv + 16 * t + 4 * q4 + r) * a.dvp] = dh[t][cc][r];
+                    to[(size_t)r * a.dvp] = dh[t][cc][r];
                     pa += h[t][cc][r] * dh[t][cc][r];
                 }
-            f32x4 x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = mma<P, S>(kf[i], hb, f32x4{0, 0, 0, 0});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[wv][i][cc][lane] = x[i];
-        }
+            }
         const float decay = end;
         pa = row_sum(decay * pa);
         if (n == 0) a.pa[((val * slices + sl) * NW + wv) * 4 + q4] = pa;
         load_a(next);
         lds_barrier();
-        f32x4 du[NI][NC], pe[NI];
-        if (work) {
+        // dU = e^(Gamma_C - Gamma) K dH' + Y^T dO
+        f32x4 du[NI][NX], pe[NI];
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = tile_of(ii);
-                pe[ii] = f32x4{0, 0, 0, 0};
+        for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    f32x4 s = ce[ii] * gather<NW>(&part[0][i][cc][lane], 4 * NC * 64);
-                    pe[ii] += s * cb[ii] * w[ii][cc];
+            for (int x = 0; x < NX; ++x) du[ii][x] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        if (st < i / 2) continue;
-                        bf16x8 d[P];
-                        get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
-                        s = mma<S, P>(yt[ii][st], d, s);
-                    }
-                    du[ii][cc] = s;
-                    put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * s);
-                    put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, ca[ii] * d_o[ii][cc]);
+        for (int s = 0; s < KS; ++s) {
+            if constexpr (!kHold) load_k(c, s, 0);
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                bf16x8 hb[S];
+                get8<S>(&hh[0][16 * deal.block(x) + n][32 * s + 8 * q4], kPh, hb);
+#pragma unroll
+                for (int ii = 0; ii < NI; ++ii) du[ii][x] = mma<P, S>(kf[ii][kHold ? s : 0], hb, du[ii][x]);
+            }
+        }
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = deal.tile(ii);
+            pe[ii] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                const int cc = deal.block(x);
+                f32x4 s = ce[ii] * du[ii][x];
+                pe[ii] += s * cb[ii] * w[ii][x];
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    if (st < i / 2) continue;
+                    bf16x8 d[P];
+                    get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
+                    s = mma<S, P>(yt[ii][st], d, s);
                 }
+                du[ii][x] = s;
+                put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * s);
+                put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, ca[ii] * d_o[ii][x]);
             }
         }
         load_b(next);
         lds_barrier();
         // dR = dU - M^T beta dU
-        if (work) {
 #pragma unroll
-            for (int ii = 0; ii < NI; ++ii) {
-                const int i = tile_of(ii);
-                f32x4 pb = {0, 0, 0, 0};
+        for (int ii = 0; ii < NI; ++ii) {
+            const int i = deal.tile(ii);
+            f32x4 pb = {0, 0, 0, 0};
 #pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    f32x4 m = {0, 0, 0, 0};
+            for (int x = 0; x < NX; ++x) {
+                const int cc = deal.block(x);
+                f32x4 m = {0, 0, 0, 0};
 #pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (s < i / 2) continue;
-                        bf16x8 u[S];
-                        get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
-                        m = mma<S, S>(tt[ii][s], u, m);
-                    }
-                    const f32x4 dr = du[ii][cc] - m, dv = cb[ii] * dr;
-                    put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -ca[ii] * dv);
-                    float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
-                        to[(size_t)r * a.dvp] = dr[r];
-                        if (row < seq.n && col < a.dv)
-                            st_io<IO>(a.dv_out.p, (size_t)((seq.row0 + row) * a.dv_out.row + hv * a.dv_out.head + col), dv[r]);
-                    }
-                    pb += dr * w[ii][cc];
+                for (int s = 0; s < 2; ++s) {
+                    if (s < i / 2) continue;
+                    bf16x8 u[S];
+                    get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                    m = mma<S, S>(tt[ii][s], u, m);
                 }
+                const f32x4 dr = du[ii][x] - m, dv = cb[ii] * dr;
+                put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -ca[ii] * dv);
+                float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) pb[r] = row_sum(pb[r]), pe[ii][r] = row_sum(pe[ii][r]);
-                if (n == 0) {
-                    const size_t at = (val * slices + sl) * kC + 16 * i + 4 * q4;
-                    *reinterpret_cast<f32x4*>(a.pb + at) = pb;
-                    *reinterpret_cast<f32x4*>(a.pe + at) = pe[ii];
+                for (int r = 0; r < 4; ++r) {
+                    const int row = c * kC + 16 * i + 4 * q4 + r, col = col0 + 16 * cc;
+                    to[(size_t)r * a.dvp] = dr[r];
+                    if (row < seq.n && col < a.dv)
+                        put_io<IO>(a.dv_out.p, (seq.row0 + row) * a.dv_out.row + hv * a.dv_out.head + col, dv[r]);
                 }
+                pb += dr * w[ii][x];
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pb[r] = row_sum(pb[r]), pe[ii][r] = row_sum(pe[ii][r]);
+            if (n == 0) {
+                // with eight waves a slice's two column blocks are two parts
+                const size_t at = ((val * slices + sl) * (NC / NX) + (NX < NC ? deal.block(0) : 0)) * kC + 16 * i + 4 * q4;
+                *reinterpret_cast<f32x4*>(a.pb + at) = pb;
+                *reinterpret_cast<f32x4*>(a.pe + at) = pe[ii];
             }
         }
         load_c(next);
@@ -805,7 +940,7 @@ __global__ void __launch_bounds__(DK * 2) rule_scan_back(const RuleArgs a) {
 // not shrink with the gate: a head that forgets at once would get its small gradient as a
 // difference of large ones.
 template <int IO, int DK>
-__global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int slices) {
+__global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts, int waves) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NT = DK / 16, NW = NT, VB = 128, LD = VB + 8;
     constexpr int S = kSum, R = kRound<IO>, D = R;  // D: terms of dH', P^T and G in dK
     constexpr int kPl = kC * LD, kSq = kC * kTp;
@@ -1034,15 +1169,15 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int slices
         }
         __syncthreads();
         if (wv == 0) {
-            const size_t at0 = val * slices;
+            const size_t at0 = val * parts;
             double own = 0, to_end = 0, lead = 0;
             float db = 0;
             for (int w = 0; w < NW; ++w) own += hs[w][lane];
-            for (int s = 0; s < slices; ++s) {
+            for (int s = 0; s < parts; ++s) {
                 to_end += a.pe[(at0 + s) * kC + lane];
                 db += a.pb[(at0 + s) * kC + lane];
             }
-            for (int s = lane; s < slices * KS * 4; s += 64) lead += a.pa[at0 * KS * 4 + s];
+            for (int s = lane; s < waves * 4; s += 64) lead += a.pa[val * waves * 4 + s];
             const double mine = to_end;
 #pragma unroll
             for (int off = 1; off < 64; off *= 2) {
@@ -1072,27 +1207,32 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int slices
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * i + 4 * q4 + r;
             if (row < ch.n && col < a.dk) {
-                st_io<IO>(a.dq.p, (size_t)((ch.row0 + row) * a.dq.row + hk * a.dq.head + col), dq[i][r]);
-                st_io<IO>(a.dk_out.p, (size_t)((ch.row0 + row) * a.dk_out.row + hk * a.dk_out.head + col), dk[i][r]);
+                put_io<IO>(a.dq.p, ((ch.row0 + row) * a.dq.row + hk * a.dq.head + col), dq[i][r]);
+                put_io<IO>(a.dk_out.p, ((ch.row0 + row) * a.dk_out.row + hk * a.dk_out.head + col), dk[i][r]);
             }
         }
 }
 
 // ------------------------------------------------------------------ launchers
 
+// Column blocks of 16 of a slice.
+template <int DK>
+constexpr int kBlocks = DK == 256 ? 2 : 1;
+
 template <int IO, int DK>
 hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
-    constexpr int NC = 1;
+    constexpr int NC = kBlocks<DK>;
     hipError_t e = hipSuccess;
     if (a.T > 0)
         e = launch(rule_prepare<IO, DK, false>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
     if (e != hipSuccess) return e;
-    return launch(rule_scan<IO, DK, NC, false>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))), dim3(DK * 2), 0, stream, a);
+    return launch(rule_scan<IO, DK, NC, false>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))),
+                  dim3(DK * 2 + 64 * kOutWaves<DK>), 0, stream, a);
 }
 
 template <int IO, int DK>
 hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
-    constexpr int NC = 1;
+    constexpr int NC = kBlocks<DK>, NW = DK / 32;
     const int slices = a.dvp / (16 * NC);
     hipError_t e = hipSuccess;
     if (a.T > 0) {
@@ -1103,7 +1243,8 @@ hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
     if (e == hipSuccess)
         e = launch(rule_scan_back<IO, DK, NC>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
     if (e == hipSuccess && a.T > 0)
-        e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a, slices);
+        e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a,
+                   slices * NC / Deal<NW, NC>::NX, slices * NW);
     return e;
 }
 

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (IO == GDN_BF16)
-                    w[i] = (uint32_t)f32_to_bf16_bits(grad(x[2 * i])) | (uint32_t)f32_to_bf16_bits(grad(x[2 * i + 1])) << 16;
+                    w[i] = (uint32_t)bf16_rne(grad(x[2 * i])) | (uint32_t)bf16_rne(grad(x[2 * i + 1])) << 16;
                 else
                     w[i] = __float_as_uint(grad(x[i]));
             }
