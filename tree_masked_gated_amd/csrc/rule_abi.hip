@@ -99,6 +99,7 @@ size_t place(RuleArgs& a, int io, int dkp, bool back, char* at) {
     take(a.qt, keys * tile);
     take(a.tt, vals * kSum * tri);
     take(a.yt, vals * kSum * tri);
+    take(a.gram, keys * 10 * 2 * 256 * sizeof(float));
     take(a.gam, vals * kC * sizeof(double));
     take(a.ht, vals * dkp * a.dvp * sizeof(float));
     take(a.dht, vals * dkp * a.dvp * sizeof(float));

@@ -55,6 +55,7 @@ struct RuleArgs {
     char* kf; char* kt; char* qf; char* qt;  // operand fragments per (slot, key head)
     char* tm; char* tt; char* ym; char* yt;  // operand fragments per (slot, value head)
     float* coef;                             // per (slot, value head): a, e^(Gamma_C - Gamma), beta [3][kC]
+    float* gram;                             // per (slot, key head): K K^T and Q K^T, tiles on and below the diagonal
     double* gam;                             // per (slot, value head): Gamma / ln 2 [kC]
     float* ht;                               // per (slot, value head): H [d_k padded][dvp]
     float* dht;                              // dH', the same layout

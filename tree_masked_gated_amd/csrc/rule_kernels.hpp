@@ -71,6 +71,14 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
             qk[j] = mma<P, P>(qfr[s].p, b, qk[j]);
         }
     }
+    if constexpr (BACK)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= wv) {
+                f32x4* to = reinterpret_cast<f32x4*>(a.gram) + (((size_t)slot * a.Hk + hk) * 10 + wv * (wv + 1) / 2 + j) * 128;
+                to[lane] = kk[j];
+                to[64 + lane] = qk[j];
+            }
     // transposed operands: 8 rows of one column per lane
     auto transposed = [&](char* to) {
         for (int t = wv; t < NT; t += 4)
@@ -303,15 +311,95 @@ struct Deal {
     __device__ int block(int x) const { return NW <= 4 ? x : wv >> 2; }
 };
 
-// Waves of the outputs.
+// The outputs' part of a scan: O = a Q H + Y U of some row tiles and column blocks.  Its operands are
+// held and requested like the state's.
+template <int IO, int DK, int NI, int NX>
+struct Outputs {
+    static constexpr int P = kPlanes<IO>, R = kRound<IO>, KS = DK / 32;
+    static constexpr bool kHold = DK * P <= 256;
+    bf16x8 qf[NI][kHold ? KS : 1][P], ym[NI][2][R];
+    f32x4 ca[NI], o[NI][NX];
+    const char *pq, *py;
+    const float* pc;
+    int64_t off[NI][4];                              // this lane's rows of a chunk of o
+    int tile[NI];
+
+    __device__ __forceinline__ void begin(const RuleArgs& a, size_t key, size_t val, int lane) {
+        pq = a.qf + key;
+        py = a.ym + val * R * kTriFrags * kFrag;
+        pc = a.coef + val * 3 * kC;
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) off[ii][r] = (16 * tile[ii] + 4 * (lane >> 4) + r) * a.o.row;
+    }
+    __device__ __forceinline__ void load_step(int s, int to, int lane) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int p = 0; p < P; ++p) qf[ii][to][p] = load_frag(pq + ((p * 4 + tile[ii]) * KS + s) * kFrag, lane);
+    }
+    __device__ __forceinline__ void load_q(int lane) {
+        if constexpr (kHold)
+#pragma unroll
+            for (int s = 0; s < KS; ++s) load_step(s, s, lane);
+    }
+    __device__ __forceinline__ void load_y(int lane) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            ca[ii] = *reinterpret_cast<const f32x4*>(pc + 16 * tile[ii] + 4 * (lane >> 4));
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int p = 0; p < R; ++p)
+                    ym[ii][s][p] = load_frag(py + (low_frag(tile[ii], min(s, tile[ii] / 2)) * R + p) * kFrag, lane);
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) o[ii][x] = f32x4{0, 0, 0, 0};
+    }
+    // += Q H for one contraction step and column block; hb: that step of H
+    template <int N>
+    __device__ __forceinline__ void add(int s, int x, const bf16x8 (&hb)[N]) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) o[ii][x] = mma<P, R>(qf[ii][kHold ? s : 0], hb, o[ii][x]);
+    }
+    // u: the column block's tile of U; to: the chunk's first row of o, this lane's column
+    __device__ __forceinline__ void finish(int x, const uint16_t* u, int plane, char* to, int rows, bool in, int lane) {
+        const int q4 = lane >> 4;
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) {
+            f32x4 y = ca[ii] * o[ii][x];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (s > tile[ii] / 2) continue;
+                bf16x8 ub[R];
+                get8<R>(u + 32 * s + 8 * q4, plane, ub);
+                y = mma<R, R>(ym[ii][s], ub, y);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (in && 16 * tile[ii] + 4 * q4 + r < rows) put_io<IO>(to, off[ii][r], y[r]);
+        }
+    }
+};
+
+// Waves of the outputs, where they have their own.
 template <int DK>
 constexpr int kOutWaves = DK / 32 < 4 ? DK / 32 : 4;
 
-template <int IO, int DK, int NC, bool BACK>
-__global__ void __launch_bounds__(DK * 2 + (BACK ? 0 : 64 * kOutWaves<DK>), IO == GDN_BF16 && DK <= 128 ? 2 : 1)
+// OUT: what becomes of the outputs.
+enum { kOutNone = 0, kOutOwn = 1, kOutSame = 2 };    // not formed; by waves of their own; by the state's waves
+
+template <int IO, int DK, int NC, int OUT>
+__global__ void __launch_bounds__(DK * 2 + (OUT == kOutOwn ? 64 * kOutWaves<DK> : 0), IO == GDN_BF16 && DK <= 128 ? 2 : 1)
 rule_scan(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
     constexpr int S = kSum, R = kRound<IO>;
+    constexpr bool BACK = OUT == kOutNone;
     typedef Deal<NW, NC> D;
     constexpr int NI = D::NI, NX = D::NX;
     constexpr bool kHold = DK * P <= 256;            // K and Q are held in registers, or read as they are used
@@ -333,109 +421,55 @@ rule_scan(const RuleArgs a) {
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
     const size_t key = ((size_t)base * a.Hk + hk) * kTile, val = (size_t)base * a.Hv + hv;
-    const size_t key_step = (size_t)a.Hk * kTile;
+    const size_t key_step = (size_t)a.Hk * kTile, y_step = (size_t)a.Hv * R * kTri;
     const float* co = a.coef + val * 3 * kC;         // of the chunk that is worked on
     const size_t co_step = (size_t)a.Hv * 3 * kC;
+    constexpr int E = IO == GDN_BF16 ? 2 : 4;
+    char* po = OUT == kOutNone ? nullptr : a.o.p + (seq.row0 * a.o.row + hv * a.o.head + col0) * E;
+    const int64_t o_step = kC * a.o.row * E;
 
-    if (!BACK && wv >= NW) {
-        // ---- the outputs: O = a Q H + Y U
+    if (OUT == kOutOwn && wv >= NW) {
         constexpr int OW = kOutWaves<DK>, OI = 4 / OW;
-        const int first = wv - NW;
-        bf16x8 qf[OI][KH][P], ym[OI][2][R];
-        f32x4 ca[OI];
-        const char* pq = a.qf + key;
-        const char* py = a.ym + val * R * kTri;
-        const float* pc = co;
-        const size_t y_step = (size_t)a.Hv * R * kTri;
-        auto load_q = [&](const char* at, int s, int to) {
+        Outputs<IO, DK, OI, NC> out;
 #pragma unroll
-            for (int ii = 0; ii < OI; ++ii)
-#pragma unroll
-                for (int p = 0; p < P; ++p)
-                    qf[ii][to][p] = load_frag(at + ((p * 4 + first + ii * OW) * KS + s) * kFrag, lane);
-        };
-        auto load = [&](bool on) {
-            if constexpr (kHold)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) load_q(pq, s, s);
-            (void)on;
-        };
-        auto load_y = [&] {
-#pragma unroll
-            for (int ii = 0; ii < OI; ++ii) {
-                const int i = first + ii * OW;
-                ca[ii] = *reinterpret_cast<const f32x4*>(pc + 16 * i + 4 * q4);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-#pragma unroll
-                    for (int p = 0; p < R; ++p)
-                        ym[ii][s][p] = load_frag(py + (low_frag(i, min(s, i / 2)) * R + p) * kFrag, lane);
-            }
-        };
-        int64_t off[OI][4];                          // this lane's rows of a chunk of o
-#pragma unroll
-        for (int ii = 0; ii < OI; ++ii)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) off[ii][r] = (16 * (first + ii * OW) + 4 * q4 + r) * a.o.row;
+        for (int ii = 0; ii < OI; ++ii) out.tile[ii] = wv - NW + ii * OW;
+        out.begin(a, key, val, lane);
         if (chunks > 0) {
-            load(true);
-            load_y();
+            out.load_q(lane);
+            out.load_y(lane);
         }
         for (int c = 0; c < chunks; ++c) {
             const bool more = c + 1 < chunks;
-            const char* pq_now = pq;
-            f32x4 o[OI][NC];
-#pragma unroll
-            for (int ii = 0; ii < OI; ++ii)
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc) o[ii][cc] = f32x4{0, 0, 0, 0};
+            out.clear();
             lds_barrier();
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                if constexpr (!kHold) load_q(pq_now, s, 0);
+                if constexpr (!kHold) out.load_step(s, 0, lane);
 #pragma unroll
                 for (int cc = 0; cc < NC; ++cc) {
                     bf16x8 hb[R];
                     get8<R>(&hh[0][16 * cc + n][32 * s + 8 * q4], kPh, hb);
-#pragma unroll
-                    for (int ii = 0; ii < OI; ++ii) o[ii][cc] = mma<P, R>(qf[ii][kHold ? s : 0], hb, o[ii][cc]);
+                    out.add(s, cc, hb);
                 }
             }
-            pq += more ? key_step : 0;
-            load(more);
+            out.pq += more ? key_step : 0;
+            out.load_q(lane);
             lds_barrier();
             lds_barrier();
-            const int rows = more ? kC : tail;
-            char* to = a.o.p + ((seq.row0 + (int64_t)c * kC) * a.o.row + hv * a.o.head) * (IO == GDN_BF16 ? 2 : 4);
 #pragma unroll
-            for (int ii = 0; ii < OI; ++ii) {
-                const int i = first + ii * OW;
-#pragma unroll
-                for (int cc = 0; cc < NC; ++cc) {
-                    f32x4 x = ca[ii] * o[ii][cc];
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) {
-                        if (s > i / 2) continue;
-                        bf16x8 u[R];
-                        get8<R>(&uu[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
-                        x = mma<R, R>(ym[ii][s], u, x);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * i + 4 * q4 + r < rows && col0 + 16 * cc < a.dv)
-                            put_io<IO>(to, off[ii][r] + col0 + 16 * cc, x[r]);
-                }
-            }
-            py += more ? y_step : 0;
-            pc += more ? co_step : 0;
-            load_y();
+            for (int cc = 0; cc < NC; ++cc)
+                out.finish(cc, &uu[0][16 * cc + n][0], kPl, po + 16 * cc * E, more ? kC : tail, col0 + 16 * cc < a.dv, lane);
+            po += o_step;
+            out.py += more ? y_step : 0;
+            out.pc += more ? co_step : 0;
+            out.load_y(lane);
         }
         return;
     }
 
     // ---- the state
     const D deal{wv};
-    __builtin_amdgcn_s_setprio(2);                   // the outputs' waves fill in
+    if constexpr (OUT == kOutOwn) __builtin_amdgcn_s_setprio(2); // the outputs' waves fill in
     // H: rows 32 wv + 16 t + 4 q4 + r, columns col0 + 16 c
     f32x4 h[2][NC];
     const size_t state = ((size_t)b * a.Hv + hv) * a.dv * a.dk;
@@ -454,6 +488,7 @@ rule_scan(const RuleArgs a) {
     bf16x8 kf[NI][KH][P], tm[NI][2][S], kt[2][2][P];
     f32x4 ca[NI], ce[NI], cb[NI];
     Rows4<IO> v[NI][NX];
+    Outputs<IO, DK, NI, NX> out;                     // kOutSame
     float end;
     const char* pk = a.kf + key;
     const char* pt = a.kt + key + 2 * wv * 2 * kFrag;
@@ -516,6 +551,15 @@ rule_scan(const RuleArgs a) {
         load_c();
         load_d();
     }
+    if constexpr (OUT == kOutSame) {
+#pragma unroll
+        for (int ii = 0; ii < NI; ++ii) out.tile[ii] = deal.tile(ii);
+        out.begin(a, key, val, lane);
+        if (chunks > 0) {
+            out.load_q(lane);
+            out.load_y(lane);
+        }
+    }
     for (int c = 0; c < chunks; ++c) {
         const bool more = c + 1 < chunks;
         const int rows = more ? kC : tail;
@@ -536,15 +580,20 @@ rule_scan(const RuleArgs a) {
         for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
             for (int x = 0; x < NX; ++x) f[ii][x] = f32x4{0, 0, 0, 0};
+        if constexpr (OUT == kOutSame) out.clear();
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            if constexpr (!kHold) load_k(pk_now, s, 0);
+            if constexpr (!kHold) {
+                load_k(pk_now, s, 0);
+                if constexpr (OUT == kOutSame) out.load_step(s, 0, lane);
+            }
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 bf16x8 hb[S];
                 get8<S>(&hh[0][16 * deal.block(x) + n][32 * s + 8 * q4], kPh, hb);
 #pragma unroll
                 for (int ii = 0; ii < NI; ++ii) f[ii][x] = mma<P, S>(kf[ii][kHold ? s : 0], hb, f[ii][x]);
+                if constexpr (OUT == kOutSame) out.add(s, x, hb);
             }
         }
 #pragma unroll
@@ -557,6 +606,10 @@ rule_scan(const RuleArgs a) {
         pk += more ? key_step : 0;
         pca += more ? co_step : 0;
         load_b(more ? c + 1 : c);
+        if constexpr (OUT == kOutSame) {
+            out.pq += more ? key_step : 0;
+            out.load_q(lane);
+        }
         lds_barrier();
         // W = F - M R, U = beta W
 #pragma unroll
@@ -603,6 +656,17 @@ rule_scan(const RuleArgs a) {
         pt += more ? key_step : 0;
         co += more ? co_step : 0;
         load_d();
+        if constexpr (OUT == kOutSame) {
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                const int cc = deal.block(x);
+                out.finish(x, &uu[0][16 * cc + n][0], kPl, po + 16 * cc * E, rows, col0 + 16 * cc < a.dv, lane);
+            }
+            po += o_step;
+            out.py += more ? y_step : 0;
+            out.pc += more ? co_step : 0;
+            out.load_y(lane);
+        }
         if constexpr (BACK) {
             ph += (size_t)a.Hv * DK * a.dvp;
             pw += (size_t)a.Hv * kC * a.dvp;
@@ -630,6 +694,25 @@ __device__ __forceinline__ float row_sum(float x) {
     x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x122, 0xf, 0xf, false));
     x += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x121, 0xf, 0xf, false));
     return x;
+}
+
+// Tile `second` of the pair of 16 x 16 blocks that stack_pair made one operand of, as accumulators lie.
+template <int P>
+__device__ __forceinline__ f32x4 rows_of_pair(const bf16x8 (&m)[P], int second) {
+    f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const u32x4 r = __builtin_bit_cast(u32x4, m[p]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const auto w = __builtin_amdgcn_permlane16_swap(r[h], r[2 + h], false, false);
+            const auto x = __builtin_amdgcn_permlane32_swap(w[0], w[1], false, false);
+            const uint32_t y = second ? x[1] : x[0];
+            v[2 * h] += __uint_as_float(y << 16);
+            v[2 * h + 1] += __uint_as_float(y & 0xffff0000u);
+        }
+    }
+    return v;
 }
 
 // Sums of the lanes up to each within a row of 16.
@@ -969,27 +1052,6 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
     for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0, 0, 0, 0};
     auto tile_row = [](int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; };
     auto tile_col = [&](int t) { return t - tile_row(t) * (tile_row(t) + 1) / 2; };
-    // K K^T and Q K^T, for Z
-    f32x4 kk[ND], qk[ND];
-#pragma unroll
-    for (int x = 0; x < ND; ++x) {
-        const int t = wv + x * NW;
-        kk[x] = qk[x] = f32x4{0, 0, 0, 0};
-        if (t >= 10) break;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            bf16x8 k[P], q[P], b[P];
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                k[p] = load_frag(a.kf + key + ((p * 4 + tile_row(t)) * KS + s) * kFrag, lane);
-                q[p] = load_frag(a.qf + key + ((p * 4 + tile_row(t)) * KS + s) * kFrag, lane);
-                b[p] = load_frag(a.kf + key + ((p * 4 + tile_col(t)) * KS + s) * kFrag, lane);
-            }
-            kk[x] = mma<P, P>(k, b, kk[x]);
-            qk[x] = mma<P, P>(q, b, qk[x]);
-        }
-    }
-
     for (int gi = 0; gi < a.group; ++gi) {
         const int hv = hk * a.group + gi;
         const size_t val = (size_t)slot * a.Hv + hv;
@@ -999,6 +1061,18 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
 #pragma unroll
         for (int i = 0; i < 4; ++i) aq[i] = t1[i] = t2[i] = f32x4{0, 0, 0, 0};
 
+        // this lane's row of H and dH': 8 value columns of a contraction step
+        const float* ph = a.ht + (val * DK + col) * a.dvp + 8 * q4;
+        const float* pd = a.dht + (val * DK + col) * a.dvp + 8 * q4;
+        f32x4 hx[2], dx2[2];
+        auto load_h = [&](int v) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                hx[j] = *reinterpret_cast<const f32x4*>(ph + v + 4 * j);
+                dx2[j] = *reinterpret_cast<const f32x4*>(pd + v + 4 * j);
+            }
+        };
+        load_h(0);
         for (int v0 = 0; v0 < a.dvp; v0 += VB) {
             const int width = min(VB, a.dvp - v0), pieces = width / 8;
             __syncthreads();
@@ -1007,35 +1081,55 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
 #pragma unroll
                 for (int x = 0; x < 3; ++x) coef[x][tid] = a.coef[(val * 3 + x) * kC + tid];
             }
-            for (int p = tid; p < kC * pieces; p += NW * 64) {
-                const int r = p / pieces, c = (p - r * pieces) * 8;
+            // U, dR and dO as operand terms; kPieces of a thread at once, all requested before any is used
+            constexpr int kPieces = kC * VB / 8 / (NW * 64);
+            f32x4 w[kPieces][2], y[kPieces][2];
+            float beta[kPieces];
+            Planes<IO> o[kPieces];
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x) {
+                const int p = min(tid + x * NW * 64, kC * pieces - 1), r = p / pieces, c = (p - r * pieces) * 8;
                 const size_t at = (val * kC + r) * a.dvp + v0 + c;
-                const float beta = a.coef[(val * 3 + 2) * kC + r];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    w[x][j] = *reinterpret_cast<const f32x4*>(a.w + at + 4 * j);
+                    y[x][j] = *reinterpret_cast<const f32x4*>(a.dr + at + 4 * j);
+                }
+                beta[x] = a.coef[(val * 3 + 2) * kC + r];
+                const bool live = r < ch.n;
+                o[x] = load_row8<IO>(a.d_o.p, (ch.row0 + (live ? r : 0)) * a.d_o.row + (int64_t)hv * a.d_o.head, v0 + c,
+                                     a.dv, a.vdo, live);
+            }
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x) {
+                const int p = tid + x * NW * 64, r = p / pieces, c = (p - r * pieces) * 8;
+                if (p >= kC * pieces) break;
                 float u[8], d[8];
 #pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const f32x4 w = *reinterpret_cast<const f32x4*>(a.w + at + j);
-                    const f32x4 y = *reinterpret_cast<const f32x4*>(a.dr + at + j);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) u[j + k] = beta * w[k], d[j + k] = y[k];
-                }
+                for (int j = 0; j < 8; ++j) u[j] = beta[x] * w[x][j / 4][j % 4], d[j] = y[x][j / 4][j % 4];
                 bf16x8 us[S], ds[S];
                 split8(u, us);
                 split8(d, ds);
 #pragma unroll
-                for (int x = 0; x < S; ++x) {
-                    *reinterpret_cast<bf16x8*>(su + x * kPl + r * LD + c) = us[x];
-                    *reinterpret_cast<bf16x8*>(sr + x * kPl + r * LD + c) = ds[x];
+                for (int t = 0; t < S; ++t) {
+                    *reinterpret_cast<bf16x8*>(su + t * kPl + r * LD + c) = us[t];
+                    *reinterpret_cast<bf16x8*>(sr + t * kPl + r * LD + c) = ds[t];
                 }
-                const bool live = r < ch.n;
-                const Planes<IO> o = load_row8<IO>(a.d_o.p, (ch.row0 + (live ? r : 0)) * a.d_o.row + (int64_t)hv * a.d_o.head,
-                                                   v0 + c, a.dv, a.vdo, live);
 #pragma unroll
-                for (int x = 0; x < P; ++x) *reinterpret_cast<bf16x8*>(so + x * kPl + r * LD + c) = o.p[x];
+                for (int t = 0; t < P; ++t) *reinterpret_cast<bf16x8*>(so + t * kPl + r * LD + c) = o[x].p[t];
             }
             __syncthreads();
             for (int s = 0; s < width / 32; ++s) {
                 const int at = 32 * s + 8 * q4;
+                bf16x8 h[S], d[D];
+                {
+                    float x[8], y[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = hx[j / 4][j % 4], y[j] = dx2[j / 4][j % 4];
+                    split8(x, h);
+                    split8(y, d);
+                }
+                load_h(min(v0 + 32 * s + 32, a.dvp - 32));
                 // dO U^T and dR U^T
 #pragma unroll
                 for (int x = 0; x < ND; ++x) {
@@ -1050,18 +1144,6 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
                     dx[x] = mma<S, S>(r, u, dx[x]);
                 }
                 // dO H^T, dR H^T and U dH'^T
-                float x[8], y[8];
-                const size_t st = (val * DK + col) * a.dvp + v0 + at;
-#pragma unroll
-                for (int j = 0; j < 8; j += 4) {
-                    const f32x4 u = *reinterpret_cast<const f32x4*>(a.ht + st + j);
-                    const f32x4 w = *reinterpret_cast<const f32x4*>(a.dht + st + j);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[j + k] = u[k], y[j + k] = w[k];
-                }
-                bf16x8 h[S], d[D];
-                split8(x, h);
-                split8(y, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     bf16x8 u[R], o[P], r[S];
@@ -1074,6 +1156,14 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
                 }
             }
         }
+        bf16x8 kt[2][P], qt[2][P];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                kt[s][p] = load_frag(a.kt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
+                qt[s][p] = load_frag(a.qt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
+            }
         __syncthreads();
         // P, its transpose, G + G^T, and the sums of Z
 #pragma unroll
@@ -1081,6 +1171,8 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             const int t = wv + x * NW;
             if (t >= 10) break;
             const int i = tile_row(t), j = tile_col(t);
+            const f32x4* gram = reinterpret_cast<const f32x4*>(a.gram) + (((size_t)slot * a.Hk + hk) * 10 + t) * 128;
+            const f32x4 kk = gram[lane], qk = gram[64 + lane];
             f32x4 p, g;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -1095,7 +1187,7 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 4 * q4 + r;
-                const float z = row_scan(i == j && n == row ? 0.f : p[r] * qk[x][r] + g[r] * kk[x][r]);
+                const float z = row_scan(i == j && n == row ? 0.f : p[r] * qk[r] + g[r] * kk[r]);
                 if (n == 15) zr[t][row] = z;
                 if (i > j || row > n) cross += z;
             }
@@ -1126,28 +1218,18 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             put4<D>(spt + (16 * j + n) * kTp + 16 * i + 4 * q4, kSq, p);
         }
         __syncthreads();
-        bf16x8 kt[2][P], qt[2][P];
-#pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-                kt[s][p] = load_frag(a.kt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
-                qt[s][p] = load_frag(a.qt + key + ((p * NT + wv) * 2 + s) * kFrag, lane);
-            }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const f32x4 ca = *reinterpret_cast<const f32x4*>(&coef[0][16 * i + 4 * q4]);
             const f32x4 ce = *reinterpret_cast<const f32x4*>(&coef[1][16 * i + 4 * q4]);
             const f32x4 cb = *reinterpret_cast<const f32x4*>(&coef[2][16 * i + 4 * q4]);
             f32x4 xq = ca * aq[i], xk = ce * t1[i] - ca * cb * t2[i];
+            const f32x4 hq = rows_of_pair(qt[i / 2], i & 1) * xq;
+            const f32x4 hk_ = rows_of_pair(kt[i / 2], i & 1) * (ca * cb * t2[i]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 4 * q4 + r;
-                const bool in = row < ch.n && col < a.dk;
-                const float q = in ? ld_io<IO>(a.q.p, (size_t)((ch.row0 + row) * a.q.row + hk * a.q.head + col)) : 0.f;
-                const float k = in ? ld_io<IO>(a.k.p, (size_t)((ch.row0 + row) * a.k.row + hk * a.k.head + col)) : 0.f;
-                const float x = row_sum(q * xq[r] - k * ca[r] * cb[r] * t2[i][r]);
-                if (n == 0) hs[wv][row] = x;
+                const float x = row_sum(hq[r] - hk_[r]);
+                if (n == 0) hs[wv][16 * i + 4 * q4 + r] = x;
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -1215,30 +1297,42 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
 
 // ------------------------------------------------------------------ launchers
 
-// Column blocks of 16 of a slice.
-template <int DK>
-constexpr int kBlocks = DK == 256 ? 2 : 1;
+// Workgroups of a scan with slices of 16 value columns.
+inline int64_t slices_of_16(const RuleArgs& a) { return (int64_t)a.B * a.Hv * (a.dvp / 16); }
 
+template <int IO, int DK, int NC, int OUT>
+hipError_t scan_launch(const RuleArgs& a, hipStream_t stream) {
+    const int waves = DK / 32 + (OUT == kOutOwn ? kOutWaves<DK> : 0);
+    return launch(rule_scan<IO, DK, NC, OUT>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))), dim3(waves * 64), 0, stream, a);
+}
+
+// Few slices, no more than two to a compute unit: the narrowest ones, and waves of their own for the
+// outputs (one sequence of 8192 rows, 32 heads, 256 slices: 251 us against 357).  Many: two column
+// blocks to a workgroup, which then reads half as many operands per column, and no waves but the
+// state's, so that two workgroups share a unit (24 prompts, 26490 rows, 6144 slices: 582 us against 863).
+constexpr int64_t kFewSlices = 512;
 template <int IO, int DK>
 hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
-    constexpr int NC = kBlocks<DK>;
     hipError_t e = hipSuccess;
     if (a.T > 0)
         e = launch(rule_prepare<IO, DK, false>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
     if (e != hipSuccess) return e;
-    return launch(rule_scan<IO, DK, NC, false>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))),
-                  dim3(DK * 2 + 64 * kOutWaves<DK>), 0, stream, a);
+    if constexpr (DK == 256) {
+        return scan_launch<IO, DK, 2, kOutSame>(a, stream);
+    } else {
+        return slices_of_16(a) <= kFewSlices ? scan_launch<IO, DK, 1, kOutOwn>(a, stream)
+                                      : scan_launch<IO, DK, 2, kOutSame>(a, stream);
+    }
 }
 
-template <int IO, int DK>
-hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
-    constexpr int NC = kBlocks<DK>, NW = DK / 32;
+template <int IO, int DK, int NC>
+hipError_t back_launch(const RuleArgs& a, hipStream_t stream) {
+    constexpr int NW = DK / 32;
     const int slices = a.dvp / (16 * NC);
     hipError_t e = hipSuccess;
     if (a.T > 0) {
         e = launch(rule_prepare<IO, DK, true>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
-        if (e == hipSuccess)
-            e = launch(rule_scan<IO, DK, NC, true>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
+        if (e == hipSuccess) e = scan_launch<IO, DK, NC, kOutNone>(a, stream);
     }
     if (e == hipSuccess)
         e = launch(rule_scan_back<IO, DK, NC>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
@@ -1246,6 +1340,14 @@ hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
         e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a,
                    slices * NC / Deal<NW, NC>::NX, slices * NW);
     return e;
+}
+
+template <int IO, int DK>
+hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
+    if constexpr (DK == 256)
+        return back_launch<IO, DK, 2>(a, stream);
+    else
+        return slices_of_16(a) <= kFewSlices ? back_launch<IO, DK, 1>(a, stream) : back_launch<IO, DK, 2>(a, stream);
 }
 
 }  // namespace gdn
