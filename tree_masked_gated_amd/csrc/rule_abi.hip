@@ -109,6 +109,8 @@ size_t place(RuleArgs& a, int io, int dkp, bool back, char* at) {
     take(a.pb, vals * slices * kC * sizeof(float));
     take(a.pe, vals * slices * kC * sizeof(float));
     take(a.pa, vals * slices * (dkp / 32) * 4 * sizeof(float));
+    take(a.hs, vals * (dkp / 16) * kC * sizeof(float));
+    take(a.zs, vals * 320 * sizeof(float));
     return used;
 }
 

@@ -16,7 +16,7 @@
 //     dQ = a dO H^T + P K,  P = lower(D o dO U^T)
 //     dK = P^T Q + (G + G^T) K + e^(Gamma_C - Gamma) U dH'^T - a beta dR H^T,
 //                                                 G = strict_lower(-beta_i D_ij dR_i . U_j)
-//     d ln g_t: rule_join says how
+//     d ln g_t: rule_join and rule_gates say how
 //
 // Both inverses come of one matrix, M = L (I + beta L)^-1: W = F - M (beta F) and
 // dR = dU - M^T (beta dU).  The unit parts stay in fp32, and a beta of 0 needs no division.
@@ -24,9 +24,10 @@
 // (the last line: d ln g_t is <P_t, dP_t>, and <S_t, dS_t> changes over a token by what the
 // token writes, v . dv, and what it reads, o . do).
 //
-// Four kernels: rule_prepare forms M and Y of all chunks at once; rule_scan walks each
+// Five kernels: rule_prepare forms M and Y of all chunks at once; rule_scan walks each
 // sequence's chunks forward, a workgroup for a slice of the value columns; rule_scan_back
-// walks them backward; rule_join forms dQ, dK and the gates' gradients of all chunks at once.
+// walks them backward; rule_join forms dQ and dK
+// of all chunks at once, and rule_gates the gates' gradients.
 #pragma once
 
 #include "attn_common.hpp"
@@ -63,6 +64,7 @@ struct RuleArgs {
     float* dr;                               // dR [kC][dvp]
     float* pb; float* pe;                    // a slice's parts of dbeta and of d ln g's terms to the end [kC]
     float* pa;                               // parts of a_C <H, dH'>, of the rows of a slice's waves
+    float* hs; float* zs;                    // rule_join's parts of d ln g: of h [kC], and sums of Z's tiles [2][10][16]
 };
 
 // Chunk slots.  Sequence b's chunks are slots base(b) .. , base(b) = offsets[b] / kC + b: the

@@ -395,7 +395,7 @@ constexpr int kOutWaves = DK / 32 < 4 ? DK / 32 : 4;
 enum { kOutNone = 0, kOutOwn = 1, kOutSame = 2 };    // not formed; by waves of their own; by the state's waves
 
 template <int IO, int DK, int NC, int OUT>
-__global__ void __launch_bounds__(DK * 2 + (OUT == kOutOwn ? 64 * kOutWaves<DK> : 0), IO == GDN_BF16 && DK <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(DK * 2 + (OUT == kOutOwn ? 64 * kOutWaves<DK> : 0), IO == GDN_BF16 && DK == 128 ? 2 : 1)
 rule_scan(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
     constexpr int S = kSum, R = kRound<IO>;
@@ -729,7 +729,7 @@ __device__ __forceinline__ float row_scan(float x) {
 // dbeta and of the terms of d ln g that reach the chunk's end: e^(Gamma_C - Gamma_j) k_j . dH' u_j
 // of every row, and a_C <H, dH'>.
 template <int IO, int DK, int NC>
-__global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 ? 2 : 1) rule_scan_back(const RuleArgs a) {
+__global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) rule_scan_back(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
     constexpr int S = kSum;
     typedef Deal<NW, NC> D;
@@ -1008,13 +1008,14 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 ? 2 : 1) rule_scan_back
 
 // ------------------------------------------------------------------ join
 //
-// dQ, dK and the gates' gradients, one workgroup per (chunk slot, key head) and d_k / 16 waves:
-// wave w owns columns 16 w .. 16 w + 15 of dQ and dK and sums them over the key head's value
+// dQ, dK and what the gates' gradients need, one workgroup per (chunk slot, key head) and d_k / 16
+// waves: wave w owns columns 16 w .. 16 w + 15 of dQ and dK and sums them over the key head's value
 // heads in registers, so that gradients of shared heads need no atomics.  The 16 x 16 tiles of
-// dO U^T and dR U^T below the diagonal are dealt to the waves; value columns go by blocks of 128.
+// dO U^T and dR U^T below the diagonal are dealt to the waves; value columns go by blocks of 64, and
+// a block's rows are requested while the block before it is worked on.
 //
-// d ln g_t is the sum of what every path across row t carries, a path from row j or from the
-// chunk's start to row i or to the chunk's end:
+// d ln g_t (rule_gates) is the sum of what every path across row t carries, a path from row j or from
+// the chunk's start to row i or to the chunk's end:
 //
 //     sum_(i >= t > j) Z_ij + sum_(i >= t) h_i + sum_(j < t) e_j + a_C <H, dH'>,
 //     Z = P o Q K^T + G o K K^T,  h_i = a_i (dO_i . H^T q_i - beta_i dR_i . H^T k_i)
@@ -1023,20 +1024,18 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 ? 2 : 1) rule_scan_back
 // not shrink with the gate: a head that forgets at once would get its small gradient as a
 // difference of large ones.
 template <int IO, int DK>
-__global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts, int waves) {
-    constexpr int P = kPlanes<IO>, KS = DK / 32, NT = DK / 16, NW = NT, VB = 128, LD = VB + 8;
+__global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a) {
+    constexpr int P = kPlanes<IO>, KS = DK / 32, NT = DK / 16, NW = NT, VB = 64, LD = VB + 8;
     constexpr int S = kSum, R = kRound<IO>, D = R;  // D: terms of dH', P^T and G in dK
     constexpr int kPl = kC * LD, kSq = kC * kTp;
     constexpr int ND = (10 + NW - 1) / NW;           // tiles below or on the diagonal, per wave
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
-    // value rows; then, in the same place, the 64 x 64 matrices
-    __shared__ __attribute__((aligned(16))) uint16_t lds[(2 * S + P) * kPl];
-    static_assert((2 * S + P) * kPl >= (S + 2 * D) * kSq, "the matrices fit");
+    // value rows of a block and, with bf16, of the next; the 64 x 64 matrices in the first one's place
+    constexpr int NB = IO == GDN_BF16 ? 2 : 1, kBlk = (2 * S + P) * kPl;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[NB * kBlk];
+    static_assert(kBlk >= (S + 2 * D) * kSq, "the matrices fit");
     __shared__ double gam[kC];
     __shared__ float coef[3][kC];
-    __shared__ float hs[NW][kC];                     // parts of h
-    __shared__ float zc[10][16], zr[10][16];         // of a tile of Z: what its row t crosses, its row sums
-    uint16_t *su = lds, *sr = lds + S * kPl, *so = sr + S * kPl;
     uint16_t *sp = lds, *spt = lds + S * kSq, *sg = spt + D * kSq;
 
     const int slot = blockIdx.x, hk = blockIdx.y;
@@ -1052,6 +1051,29 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
     for (int i = 0; i < 4; ++i) dq[i] = dk[i] = f32x4{0, 0, 0, 0};
     auto tile_row = [](int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; };
     auto tile_col = [&](int t) { return t - tile_row(t) * (tile_row(t) + 1) / 2; };
+    // rows of U (as W), dR and dO of one block: 8 columns of a row to a thread
+    constexpr int kPiecesAll = kC * VB / 8, kPieces = (kPiecesAll + NW * 64 - 1) / (NW * 64);
+    f32x4 bw[kPieces][2], by[kPieces][2];
+    float bb[kPieces];
+    Planes<IO> bo[kPieces];
+    auto load_block = [&](int hv, int v0) {
+        const size_t val = (size_t)slot * a.Hv + hv;
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+            const int p = min(tid + x * NW * 64, kPiecesAll - 1), r = p / (VB / 8), c = min(v0 + p % (VB / 8) * 8, a.dvp - 8);
+            const size_t at = (val * kC + r) * a.dvp + c;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                bw[x][j] = *reinterpret_cast<const f32x4*>(a.w + at + 4 * j);
+                by[x][j] = *reinterpret_cast<const f32x4*>(a.dr + at + 4 * j);
+            }
+            bb[x] = a.coef[(val * 3 + 2) * kC + r];
+            const bool live = r < ch.n;
+            bo[x] = load_row8<IO>(a.d_o.p, (ch.row0 + (live ? r : 0)) * a.d_o.row + (int64_t)hv * a.d_o.head, c, a.dv,
+                                  a.vdo, live);
+        }
+    };
+    load_block(hk * a.group, 0);
     for (int gi = 0; gi < a.group; ++gi) {
         const int hv = hk * a.group + gi;
         const size_t val = (size_t)slot * a.Hv + hv;
@@ -1074,39 +1096,22 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
         };
         load_h(0);
         for (int v0 = 0; v0 < a.dvp; v0 += VB) {
-            const int width = min(VB, a.dvp - v0), pieces = width / 8;
-            __syncthreads();
+            const int width = min(VB, a.dvp - v0);
+            uint16_t* su = lds + (NB == 2 ? v0 / VB % 2 : 0) * kBlk;
+            uint16_t *sr = su + S * kPl, *so = sr + S * kPl;
+            if (NB == 1 || v0 == 0) __syncthreads();
             if (v0 == 0 && tid < kC) {
                 gam[tid] = a.gam[val * kC + tid];
 #pragma unroll
                 for (int x = 0; x < 3; ++x) coef[x][tid] = a.coef[(val * 3 + x) * kC + tid];
             }
-            // U, dR and dO as operand terms; kPieces of a thread at once, all requested before any is used
-            constexpr int kPieces = kC * VB / 8 / (NW * 64);
-            f32x4 w[kPieces][2], y[kPieces][2];
-            float beta[kPieces];
-            Planes<IO> o[kPieces];
 #pragma unroll
             for (int x = 0; x < kPieces; ++x) {
-                const int p = min(tid + x * NW * 64, kC * pieces - 1), r = p / pieces, c = (p - r * pieces) * 8;
-                const size_t at = (val * kC + r) * a.dvp + v0 + c;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    w[x][j] = *reinterpret_cast<const f32x4*>(a.w + at + 4 * j);
-                    y[x][j] = *reinterpret_cast<const f32x4*>(a.dr + at + 4 * j);
-                }
-                beta[x] = a.coef[(val * 3 + 2) * kC + r];
-                const bool live = r < ch.n;
-                o[x] = load_row8<IO>(a.d_o.p, (ch.row0 + (live ? r : 0)) * a.d_o.row + (int64_t)hv * a.d_o.head, v0 + c,
-                                     a.dv, a.vdo, live);
-            }
-#pragma unroll
-            for (int x = 0; x < kPieces; ++x) {
-                const int p = tid + x * NW * 64, r = p / pieces, c = (p - r * pieces) * 8;
-                if (p >= kC * pieces) break;
+                const int p = tid + x * NW * 64, r = p / (VB / 8), c = p % (VB / 8) * 8;
+                if (kPiecesAll % (NW * 64) != 0 && p >= kPiecesAll) break;
                 float u[8], d[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) u[j] = beta[x] * w[x][j / 4][j % 4], d[j] = y[x][j / 4][j % 4];
+                for (int j = 0; j < 8; ++j) u[j] = bb[x] * bw[x][j / 4][j % 4], d[j] = by[x][j / 4][j % 4];
                 bf16x8 us[S], ds[S];
                 split8(u, us);
                 split8(d, ds);
@@ -1116,9 +1121,13 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
                     *reinterpret_cast<bf16x8*>(sr + t * kPl + r * LD + c) = ds[t];
                 }
 #pragma unroll
-                for (int t = 0; t < P; ++t) *reinterpret_cast<bf16x8*>(so + t * kPl + r * LD + c) = o[x].p[t];
+                for (int t = 0; t < P; ++t) *reinterpret_cast<bf16x8*>(so + t * kPl + r * LD + c) = bo[x].p[t];
             }
             __syncthreads();
+            {
+                const bool same = v0 + VB < a.dvp;   // the next block, or the last one again
+                load_block(same || gi + 1 == a.group ? hv : hv + 1, same ? v0 + VB : 0);
+            }
             for (int s = 0; s < width / 32; ++s) {
                 const int at = 32 * s + 8 * q4;
                 bf16x8 h[S], d[D];
@@ -1146,15 +1155,25 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
                 // dO H^T, dR H^T and U dH'^T
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    const int row = (16 * i + n) * LD + at;
                     bf16x8 u[R], o[P], r[S];
-                    get8<R>(su + (16 * i + n) * LD + at, kPl, u);
-                    get8<P>(so + (16 * i + n) * LD + at, kPl, o);
-                    get8<S>(sr + (16 * i + n) * LD + at, kPl, r);
+                    get8<R>(su + row, kPl, u);
+                    get8<P>(so + row, kPl, o);
+                    get8<S>(sr + row, kPl, r);
                     aq[i] = mma<P, S>(o, h, aq[i]);
                     t2[i] = mma<S, S>(r, h, t2[i]);
                     t1[i] = mma<R, D>(u, d, t1[i]);
                 }
             }
+        }
+        // requested before the barrier: the products that Z takes, and the operands of P and G
+        f32x4 kk[ND], qk[ND];
+#pragma unroll
+        for (int x = 0; x < ND; ++x) {
+            const f32x4* gram =
+                reinterpret_cast<const f32x4*>(a.gram) + (((size_t)slot * a.Hk + hk) * 10 + min(wv + x * NW, 9)) * 128;
+            kk[x] = gram[lane];
+            qk[x] = gram[64 + lane];
         }
         bf16x8 kt[2][P], qt[2][P];
 #pragma unroll
@@ -1171,8 +1190,6 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             const int t = wv + x * NW;
             if (t >= 10) break;
             const int i = tile_row(t), j = tile_col(t);
-            const f32x4* gram = reinterpret_cast<const f32x4*>(a.gram) + (((size_t)slot * a.Hk + hk) * 10 + t) * 128;
-            const f32x4 kk = gram[lane], qk = gram[64 + lane];
             f32x4 p, g;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -1184,17 +1201,17 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             // z: the sums of Z's columns up to this one; of column 15, of the whole row.  Row t = 16 j + n + 1
             // is crossed by the rows i >= t of them.
             float cross = 0.f;
+            float* zs = a.zs + val * 320 + 16 * t;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 4 * q4 + r;
-                const float z = row_scan(i == j && n == row ? 0.f : p[r] * qk[r] + g[r] * kk[r]);
-                if (n == 15) zr[t][row] = z;
+                const float z = row_scan(i == j && n == row ? 0.f : p[r] * qk[x][r] + g[r] * kk[x][r]);
+                if (n == 15) zs[160 + row] = z;
                 if (i > j || row > n) cross += z;
             }
             cross += __shfl_xor(cross, 16);
             cross += __shfl_xor(cross, 32);
-            if (q4 == 0 && n < 15) zc[t][n + 1] = cross;
-            if (lane == 0) zc[t][0] = 0.f;
+            if (q4 == 0) zs[n < 15 ? n + 1 : 0] = n < 15 ? cross : 0.f;
             s16x4 ps[S], gs[D];
             split4p(p, ps);
             split4p(g, gs);
@@ -1223,14 +1240,9 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             const f32x4 ca = *reinterpret_cast<const f32x4*>(&coef[0][16 * i + 4 * q4]);
             const f32x4 ce = *reinterpret_cast<const f32x4*>(&coef[1][16 * i + 4 * q4]);
             const f32x4 cb = *reinterpret_cast<const f32x4*>(&coef[2][16 * i + 4 * q4]);
-            f32x4 xq = ca * aq[i], xk = ce * t1[i] - ca * cb * t2[i];
-            const f32x4 hq = rows_of_pair(qt[i / 2], i & 1) * xq;
-            const f32x4 hk_ = rows_of_pair(kt[i / 2], i & 1) * (ca * cb * t2[i]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float x = row_sum(hq[r] - hk_[r]);
-                if (n == 0) hs[wv][16 * i + 4 * q4 + r] = x;
-            }
+            const f32x4 back = ca * cb * t2[i];
+            f32x4 xq = ca * aq[i], xk = ce * t1[i] - back;
+            f32x4 h = rows_of_pair(qt[i / 2], i & 1) * xq - rows_of_pair(kt[i / 2], i & 1) * back;
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int at = (16 * i + n) * kTp + 32 * s + 8 * q4;
@@ -1248,39 +1260,9 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
             }
             dq[i] += xq;
             dk[i] += xk;
-        }
-        __syncthreads();
-        if (wv == 0) {
-            const size_t at0 = val * parts;
-            double own = 0, to_end = 0, lead = 0;
-            float db = 0;
-            for (int w = 0; w < NW; ++w) own += hs[w][lane];
-            for (int s = 0; s < parts; ++s) {
-                to_end += a.pe[(at0 + s) * kC + lane];
-                db += a.pb[(at0 + s) * kC + lane];
-            }
-            for (int s = lane; s < waves * 4; s += 64) lead += a.pa[val * waves * 4 + s];
-            const double mine = to_end;
 #pragma unroll
-            for (int off = 1; off < 64; off *= 2) {
-                const double y = __shfl_down(own, off), z = __shfl_up(to_end, off);
-                if (lane + off < 64) own += y;
-                if (lane >= off) to_end += z;
-                lead += __shfl_xor(lead, off);
-            }
-            double d = lead + own + to_end - mine;
-            const int T = q4;                        // row t = 16 T + n
-            for (int t = 0; t < 10; ++t) {
-                const int i = tile_row(t), j = tile_col(t);
-                if (j == T) d += zc[t][n];
-                if (j < T && T <= i)
-                    for (int r = T == i ? n : 0; r < 16; ++r) d += zr[t][r];
-            }
-            if (lane < ch.n) {
-                const int64_t at = (ch.row0 + lane) * a.Hv + hv;
-                a.dlog_g[at] = (float)d;
-                a.dbeta[at] = db;
-            }
+            for (int r = 0; r < 4; ++r) h[r] = row_sum(h[r]);
+            if (n == 0) *reinterpret_cast<f32x4*>(a.hs + (val * NT + wv) * kC + 16 * i + 4 * q4) = h;
         }
     }
 #pragma unroll
@@ -1289,10 +1271,52 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a, int parts,
         for (int r = 0; r < 4; ++r) {
             const int row = 16 * i + 4 * q4 + r;
             if (row < ch.n && col < a.dk) {
-                put_io<IO>(a.dq.p, ((ch.row0 + row) * a.dq.row + hk * a.dq.head + col), dq[i][r]);
-                put_io<IO>(a.dk_out.p, ((ch.row0 + row) * a.dk_out.row + hk * a.dk_out.head + col), dk[i][r]);
+                put_io<IO>(a.dq.p, (ch.row0 + row) * a.dq.row + hk * a.dq.head + col, dq[i][r]);
+                put_io<IO>(a.dk_out.p, (ch.row0 + row) * a.dk_out.row + hk * a.dk_out.head + col, dk[i][r]);
             }
         }
+}
+
+// The gates' gradients of one (chunk slot, value head): a wave, lane t for row t.  parts and waves:
+// what a slice's waves left in pb and pe, and in pa; hsums: in hs.
+template <int IO>
+__global__ void __launch_bounds__(64) rule_gates(const RuleArgs a, int parts, int waves, int hsums) {
+    const int slot = blockIdx.x, hv = blockIdx.y, lane = threadIdx.x;
+    const RuleChunk ch = rule_chunk(a, slot);
+    if (ch.n == 0) return;
+    const size_t val = (size_t)slot * a.Hv + hv;
+    __shared__ float z[320];
+    for (int i = lane; i < 320; i += 64) z[i] = a.zs[val * 320 + i];
+    double own = 0, to_end = 0, lead = 0;
+    float db = 0;
+    for (int w = 0; w < hsums; ++w) own += a.hs[(val * hsums + w) * kC + lane];
+    for (int s = 0; s < parts; ++s) {
+        to_end += a.pe[(val * parts + s) * kC + lane];
+        db += a.pb[(val * parts + s) * kC + lane];
+    }
+    for (int s = lane; s < waves * 4; s += 64) lead += a.pa[val * waves * 4 + s];
+    const double mine = to_end;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+        const double y = __shfl_down(own, off), x = __shfl_up(to_end, off);
+        if (lane + off < 64) own += y;
+        if (lane >= off) to_end += x;
+        lead += __shfl_xor(lead, off);
+    }
+    double d = lead + own + to_end - mine;
+    __syncthreads();
+    const int T = lane / 16, n = lane % 16;
+    for (int t = 0; t < 10; ++t) {
+        const int i = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, j = t - i * (i + 1) / 2;
+        if (j == T) d += z[16 * t + n];
+        if (j < T && T <= i)
+            for (int r = T == i ? n : 0; r < 16; ++r) d += z[160 + 16 * t + r];
+    }
+    if (lane < ch.n) {
+        const int64_t at = (ch.row0 + lane) * a.Hv + hv;
+        a.dlog_g[at] = (float)d;
+        a.dbeta[at] = db;
+    }
 }
 
 // ------------------------------------------------------------------ launchers
@@ -1336,9 +1360,12 @@ hipError_t back_launch(const RuleArgs& a, hipStream_t stream) {
     }
     if (e == hipSuccess)
         e = launch(rule_scan_back<IO, DK, NC>, dim3(a.B * a.Hv * slices), dim3(DK * 2), 0, stream, a);
-    if (e == hipSuccess && a.T > 0)
-        e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a,
-                   slices * NC / Deal<NW, NC>::NX, slices * NW);
+    if (e == hipSuccess && a.T > 0) {
+        e = launch(rule_join<IO, DK>, dim3(a.n_slots, a.Hk), dim3(DK * 4), 0, stream, a);
+        if (e == hipSuccess)
+            e = launch(rule_gates<IO>, dim3(a.n_slots, a.Hv), dim3(64), 0, stream, a, slices * NC / Deal<NW, NC>::NX,
+                       slices * NW, DK / 16);
+    }
     return e;
 }
 
