@@ -1,15 +1,17 @@
 // score.hip -- log-probabilities of given tokens, entropy and best alternatives of rows of
 // logits, and their gradient; kernels and C ABI.
 //
-// One pass over a row keeps, per thread, the running maximum m, s = sum e^(x - m) and
-// t = sum e^(x - m) (x - m); a change of m by d turns them into e^d s and e^d (t + d s).  Then
-// lse = m + ln s and the entropy is ln s - t / s.  Both kernels are bound by the logits' bytes.
+// One pass over a row keeps, per thread, the running maximum m and, with d = (x - m) log2 e, s = sum
+// 2^d and t = sum 2^d d; a change of m by d turns them into 2^d s and 2^d (t + d s).  Then lse = m +
+// ln s and the entropy is ln s - (t / s) ln 2.  Both kernels are bound by the logits' bytes; the
+// exponentials and sums take two thirds of that time.
 //
-// Best alternatives come of the threads' maxima: with the threads in at least k groups, the least
-// of the groups' maxima is a bound that at least k elements reach, and on most rows few more
-// (about g ln g of g groups).  Threads whose own maximum reaches it read their elements once
-// more; what reaches it is ordered by counting.  Where more elements reach it than fit, as in
-// rows that are masked nearly everywhere, the k-th best is found byte by byte of (value, index).
+// The best alternative is in the piece of 16 bytes where its thread last raised its maximum.  More
+// alternatives come of a bound that at least k of the threads' maxima reach: the least maximum of
+// eight groups of threads, or, past eight, one found by halving that few more than k reach.  Threads
+// whose own maximum reaches it read their elements once more; what reaches it is ordered by
+// counting.  Where more elements reach it than fit, as in rows that are masked nearly
+// everywhere, the k-th best is found byte by byte of (value, index).
 #include <float.h>
 #include <stdint.h>
 
@@ -21,7 +23,7 @@ namespace gdn {
 namespace {
 
 constexpr int kMaxTop = 64;
-constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // What stands in for -inf where it would meet a factor of 0.
 constexpr float kFar = -1e30f;
 
@@ -72,16 +74,24 @@ struct Span {
     }
     __device__ int first_of(int p) const { return lo + head + p * kPer<IO>; }
     __device__ int tail() const { return first_of(pieces); }
-    // f(x, index) for this thread's elements
+    // f(x, index) for this thread's elements; four pieces are requested at once
     template <class F>
     __device__ void each(int threads, F f) const {
         const int t = threadIdx.x;
         if (t < head) f(ld_io<IO>(row, lo + t), lo + t);
-        for (int p = t; p < pieces; p += threads) {
-            float x[kPer<IO>];
-            unpack<IO>(*piece(p), x);
+        for (int p0 = t; p0 < pieces; p0 += 4 * threads) {
+            u32x4 v[4];
 #pragma unroll
-            for (int i = 0; i < kPer<IO>; ++i) f(x[i], first_of(p) + i);
+            for (int u = 0; u < 4; ++u) v[u] = *piece(min(p0 + u * threads, pieces - 1));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int p = p0 + u * threads;
+                if (p >= pieces) break;
+                float x[kPer<IO>];
+                unpack<IO>(v[u], x);
+#pragma unroll
+                for (int i = 0; i < kPer<IO>; ++i) f(x[i], first_of(p) + i);
+            }
         }
         if (t < hi - tail()) f(ld_io<IO>(row, tail() + t), tail() + t);
     }
@@ -90,15 +100,15 @@ struct Span {
 struct Stat {
     float m, s, t;
     __device__ void raise(float to) {        // to >= m
-        const float d = fmaxf(m - to, kFar), e = exp2f(d * kLog2E);
+        const float d = fmaxf((m - to) * kLog2E, kFar), e = __builtin_amdgcn_exp2f(d);
         t = e * (t + d * s);
         s = e * s;
         m = to;
     }
     __device__ void add(float x) {           // x <= m
-        const float d = x - m, e = exp2f(d * kLog2E);
+        const float d = (x - m) * kLog2E, e = __builtin_amdgcn_exp2f(d);
         s += e;
-        t += e * fmaxf(d, kFar);
+        t = fmaf(e, fmaxf(d, kFar), t);
     }
     __device__ void join(Stat o) {
         const float to = fmaxf(m, o.m);
@@ -108,7 +118,6 @@ struct Stat {
         t += o.t;
     }
 };
-
 // Floats as unsigned numbers in the same order: -0 is 0, NaN is above all.
 __device__ __forceinline__ uint32_t order_of(float x) {
     const uint32_t u = __float_as_uint(x + 0.f);
@@ -127,10 +136,9 @@ __device__ __forceinline__ int index_of(uint64_t r) { return 0xffffff - (int)(r 
 struct Row {
     float m, log_s, mean;
     __device__ explicit Row(const Stat& a) {
-        const float nan = __builtin_nanf("");
-        m = a.s == 0.f ? nan : a.m;          // no finite logit
+        m = a.s == 0.f ? __builtin_nanf("") : a.m; // no finite logit
         log_s = logf(a.s);
-        mean = a.t / a.s;
+        mean = a.t / a.s * kLn2;
     }
     __device__ float logp(float x) const { return (x - m) - log_s; }
 };
@@ -161,7 +169,8 @@ template <int IO, int NT>
 __global__ void __launch_bounds__(NT) score_rows(const ScoreArgs a) {
     constexpr int NW = NT / 64, U = 4, kCap = 512;
     __shared__ Stat stats[NW];
-    __shared__ uint32_t lows[NW];
+    __shared__ uint32_t lows[NW], highs[NW];
+    __shared__ int reach[2][NW];
     __shared__ uint64_t cand[kCap];
     __shared__ uint32_t hist[256];
     __shared__ int count;
@@ -171,34 +180,37 @@ __global__ void __launch_bounds__(NT) score_rows(const ScoreArgs a) {
     const Span<IO> sp(a.logits + (size_t)(row * a.stride) * (IO == GDN_BF16 ? 2 : 4), part * a.part,
                       min(a.vocab, (part + 1) * a.part));
     Stat st{-FLT_MAX, 0.f, 0.f};
-    if (tid < sp.head) {
-        const float x = ld_io<IO>(sp.row, sp.lo + tid);
-        st.raise(fmaxf(st.m, x));
+    int where = -1;                                  // of the maximum: a piece; or a single element, before or after
+    auto single = [&](float x, int at) {
+        if (x > st.m) {
+            st.raise(x);
+            where = at;
+        }
         st.add(x);
-    }
-    if (tid < sp.hi - sp.tail()) {
-        const float x = ld_io<IO>(sp.row, sp.tail() + tid);
-        st.raise(fmaxf(st.m, x));
-        st.add(x);
-    }
+    };
+    if (tid < sp.head) single(ld_io<IO>(sp.row, sp.lo + tid), -1);
     for (int p0 = tid; p0 < sp.pieces; p0 += NT * U) {
         u32x4 v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (p0 + u * NT < sp.pieces) v[u] = *sp.piece(p0 + u * NT);
+        for (int u = 0; u < U; ++u) v[u] = *sp.piece(min(p0 + u * NT, sp.pieces - 1));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (p0 + u * NT >= sp.pieces) break;
+            const int p = p0 + u * NT;
+            if (p >= sp.pieces) break;
             float x[kPer<IO>];
             unpack<IO>(v[u], x);
-            float to = st.m;
+            float to = x[0];
 #pragma unroll
-            for (int i = 0; i < kPer<IO>; ++i) to = fmaxf(to, x[i]);
-            if (to > st.m) st.raise(to);
+            for (int i = 1; i < kPer<IO>; ++i) to = fmaxf(to, x[i]);
+            if (to > st.m) {
+                st.raise(to);
+                where = p;
+            }
 #pragma unroll
             for (int i = 0; i < kPer<IO>; ++i) st.add(x[i]);
         }
     }
+    if (tid < sp.hi - sp.tail()) single(ld_io<IO>(sp.row, sp.tail() + tid), -2);
     // a thread that saw NaN (its sum is) has an element above all
     const uint32_t mine = st.s != st.s ? 0xffffffffu : order_of(st.m);
     const int topk = a.topk;
@@ -206,7 +218,11 @@ __global__ void __launch_bounds__(NT) score_rows(const ScoreArgs a) {
     int width = 64;                                  // lanes of a group
     while (topk > 1 && NT / width < topk) width /= 2;
     for (int off = 1; off < width; off *= 2) low = max(low, (uint32_t)__shfl_xor((int)low, off));
-    for (int off = width; off < 64; off *= 2) low = min(low, (uint32_t)__shfl_xor((int)low, off));
+    uint32_t high = low;                             // of all threads
+    for (int off = width; off < 64; off *= 2) {
+        low = min(low, (uint32_t)__shfl_xor((int)low, off));
+        high = max(high, (uint32_t)__shfl_xor((int)high, off));
+    }
 #pragma unroll
     for (int off = 1; off < 64; off *= 2) {
         Stat o;
@@ -215,23 +231,52 @@ __global__ void __launch_bounds__(NT) score_rows(const ScoreArgs a) {
         o.t = __shfl_xor(st.t, off);
         st.join(o);
     }
-    if (lane == 0) stats[wv] = st, lows[wv] = low;
+    if (lane == 0) stats[wv] = st, lows[wv] = low, highs[wv] = high;
     if (tid == 0) count = 0;
     __syncthreads();
     st = stats[0];
     low = lows[0];
+    high = highs[0];
 #pragma unroll
     for (int w = 1; w < NW; ++w) {
         st.join(stats[w]);
-        low = topk > 1 ? min(low, lows[w]) : max(low, lows[w]);
+        low = min(low, lows[w]);
+        high = max(high, highs[w]);
     }
     if (topk > 0) {
-        if (mine >= low)
-            sp.each(NT, [&](float x, int i) {
-                if (order_of(x) < low) return;
-                const int at = atomicAdd(&count, 1);
-                if (at < kCap) cand[at] = rank_of(x, i);
-            });
+        if (topk == 1) low = high;
+        // past eight groups their least maximum is far below the k-th of all: low's reach, at least
+        // topk threads, is halved until few more are left
+        if (topk > 8)
+            for (int step = 0; step < 20 && high - low > 1; ++step) {
+                const uint32_t mid = low + (high - low) / 2;
+                const int have = __popcll(__ballot(mine >= mid));
+                if (lane == 0) reach[step & 1][wv] = have;
+                __syncthreads();
+                int all = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) all += reach[step & 1][w];
+                if (all >= topk) low = mid; else high = mid;
+                if (all >= topk && all <= topk + topk / 4) break;
+            }
+        auto keep = [&](float x, int i) {
+            if (order_of(x) < low) return;
+            const int at = atomicAdd(&count, 1);
+            if (at < kCap) cand[at] = rank_of(x, i);
+        };
+        if (mine >= low) {
+            if (topk > 1 || low == 0xffffffffu) {
+                sp.each(NT, keep);
+            } else if (where < 0) {
+                const int i = where == -1 ? sp.lo + tid : sp.tail() + tid;
+                if (i < sp.hi) keep(ld_io<IO>(sp.row, i), i);
+            } else {
+                float x[kPer<IO>];
+                unpack<IO>(*sp.piece(where), x);
+#pragma unroll
+                for (int i = 0; i < kPer<IO>; ++i) keep(x[i], sp.first_of(where) + i);
+            }
+        }
         __syncthreads();
         int n = count;
         __syncthreads();
@@ -363,7 +408,7 @@ __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
     for (int i = 0; i < points; ++i) all += add[i];
     const float ge = a.d_entropy ? a.d_entropy[row] : 0.f, h = a.d_entropy ? a.entropy[row] : 0.f, lse = a.lse[row];
     auto grad = [&](float x) {
-        const float l = x - lse, p = exp2f(l * kLog2E);
+        const float l = x - lse, p = __builtin_amdgcn_exp2f(l * kLog2E);
         return -p * (all + ge * (fmaxf(l, kFar) + h));
     };
     if (tid < sp.head) st_io<IO>(out, sp.lo + tid, grad(ld_io<IO>(sp.row, sp.lo + tid)));
