@@ -751,50 +751,74 @@ def rule_workspace(d: RuleDims, n_rows, backward=False, device="cuda"):
     return torch.empty(max(gdn_rule_workspace_bytes(d, n_rows, backward), 16), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=None)
+def _rule_bytes_of(sizes, T, backward):
+    return gdn_rule_workspace_bytes(RuleDims(*sizes), T, backward)
+
+
 def _rule_workspace(ws, d, T, backward):
-    need = gdn_rule_workspace_bytes(d, T, backward)
-    if ws.dtype != torch.uint8 or not ws.is_cuda or not ws.is_contiguous() or ws.numel() < need:
+    need = _rule_bytes_of((d.batch, d.h_k, d.h_v, d.d_k, d.d_v, d.io_dtype), T, backward)
+    if ws.dtype is not torch.uint8 or ws.numel() < need or not ws.is_cuda or not ws.is_contiguous():
         raise ValueError(f"workspace: expected {need} contiguous bytes or more (rule_workspace)")
     return ws.data_ptr()
 
 
+_f32 = torch.float32
+
+
+def _f32s(x, shape, name):
+    """Device pointer of a contiguous float32 tensor of this shape; None gives NULL."""
+    if x is None:
+        return None
+    if x.dtype is not _f32 or x.shape != shape or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous float32 device tensor of shape {tuple(shape)}, "
+                         f"got {x.dtype} {tuple(x.shape)}")
+    return x.data_ptr()
+
+
 def gdn_rule_forward(d: RuleDims, offsets, q, k, v, beta, g, o, workspace, S0=None, S_out=None, stream=None) -> None:
     """Enqueue the rule along every sequence (see gdn_rule.h): o, and the states after the sequences."""
-    T, io, state = q.shape[0], _io_dtype(d), (d.batch, d.h_v, d.d_v, d.d_k)
-    _call("gdn_rule_forward", ctypes.byref(d), _ints(offsets, (d.batch + 1,), "offsets"), T,
-          _ptr(S0, state, torch.float32, "S0"), _attn_rows(q, T, d.h_k, d.d_k, io, "q"),
-          _attn_rows(k, T, d.h_k, d.d_k, io, "k"), _attn_rows(v, T, d.h_v, d.d_v, io, "v"),
-          _ptr(beta, (T, d.h_v), torch.float32, "beta"), _ptr(g, (T, d.h_v), torch.float32, "g"),
-          _attn_rows(o, T, d.h_v, d.d_v, io, "o"), _ptr(S_out, state, torch.float32, "S_out"),
-          _rule_workspace(workspace, d, T, False), _stream(stream))
+    B, hk, hv, dk, dv = d.batch, d.h_k, d.h_v, d.d_k, d.d_v
+    T, io, state = q.shape[0], _io_dtype(d), (B, hv, dv, dk)
+    rc = _lib.gdn_rule_forward(
+        d, _ints(offsets, (B + 1,), "offsets"), T, _f32s(S0, state, "S0"), _attn_rows(q, T, hk, dk, io, "q"),
+        _attn_rows(k, T, hk, dk, io, "k"), _attn_rows(v, T, hv, dv, io, "v"), _f32s(beta, (T, hv), "beta"),
+        _f32s(g, (T, hv), "g"), _attn_rows(o, T, hv, dv, io, "o"), _f32s(S_out, state, "S_out"),
+        _rule_workspace(workspace, d, T, False), _stream(stream))
+    if rc:
+        raise GdnError(rc, "gdn_rule_forward")
 
 
 def gdn_rule_backward(d: RuleDims, offsets, q, k, v, beta, g, d_o, dq, dk, dv, dbeta, dlog_g, workspace, S0=None,
                       dS_out=None, dS0=None, stream=None) -> None:
     """Enqueue the gradients of gdn_rule_forward (see gdn_rule.h), from its inputs alone.  dlog_g is the
     gradient with regard to ln g."""
-    T, io, state = q.shape[0], _io_dtype(d), (d.batch, d.h_v, d.d_v, d.d_k)
-    keys = lambda x, name: _attn_rows(x, T, d.h_k, d.d_k, io, name)  # noqa: E731
-    vals = lambda x, name: _attn_rows(x, T, d.h_v, d.d_v, io, name)  # noqa: E731
-    gate = lambda x, name: _ptr(x, (T, d.h_v), torch.float32, name)  # noqa: E731
-    _call("gdn_rule_backward", ctypes.byref(d), _ints(offsets, (d.batch + 1,), "offsets"), T,
-          _ptr(S0, state, torch.float32, "S0"), keys(q, "q"), keys(k, "k"), vals(v, "v"), gate(beta, "beta"),
-          gate(g, "g"), vals(d_o, "d_o"), _ptr(dS_out, state, torch.float32, "dS_out"), keys(dq, "dq"),
-          keys(dk, "dk"), vals(dv, "dv"), gate(dbeta, "dbeta"), gate(dlog_g, "dlog_g"),
-          _ptr(dS0, state, torch.float32, "dS0"), _rule_workspace(workspace, d, T, True), _stream(stream))
+    B, h_k, h_v = d.batch, d.h_k, d.h_v
+    T, io, state = q.shape[0], _io_dtype(d), (B, h_v, d.d_v, d.d_k)
+    keys = lambda x, name: _attn_rows(x, T, h_k, d.d_k, io, name)  # noqa: E731
+    vals = lambda x, name: _attn_rows(x, T, h_v, d.d_v, io, name)  # noqa: E731
+    gate = (T, h_v)
+    rc = _lib.gdn_rule_backward(
+        d, _ints(offsets, (B + 1,), "offsets"), T, _f32s(S0, state, "S0"), keys(q, "q"), keys(k, "k"), vals(v, "v"),
+        _f32s(beta, gate, "beta"), _f32s(g, gate, "g"), vals(d_o, "d_o"), _f32s(dS_out, state, "dS_out"),
+        keys(dq, "dq"), keys(dk, "dk"), vals(dv, "dv"), _f32s(dbeta, gate, "dbeta"), _f32s(dlog_g, gate, "dlog_g"),
+        _f32s(dS0, state, "dS0"), _rule_workspace(workspace, d, T, True), _stream(stream))
+    if rc:
+        raise GdnError(rc, "gdn_rule_backward")
 
 
 def gdn_rule_step(d: RuleDims, q, k, v, beta, g, state, o, slot=None, stream=None) -> None:
     """Enqueue one token of every sequence on a pool of states [slots, h_v, d_v, d_k], in place (see
     gdn_rule.h).  slot: each sequence's place in the pool (-1: none), or None for its own number."""
-    B, io = d.batch, _io_dtype(d)
-    gate = lambda x, name: _ptr(x, (B, d.h_v), torch.float32, name)  # noqa: E731
-    n = state.shape[0]
-    _call("gdn_rule_step", ctypes.byref(d), None if slot is None else _ints(slot, (B,), "slot"), n,
-          _attn_rows(q, B, d.h_k, d.d_k, io, "q"), _attn_rows(k, B, d.h_k, d.d_k, io, "k"),
-          _attn_rows(v, B, d.h_v, d.d_v, io, "v"), gate(beta, "beta"), gate(g, "g"),
-          _ptr(state, (n, d.h_v, d.d_v, d.d_k), torch.float32, "state"), _attn_rows(o, B, d.h_v, d.d_v, io, "o"),
-          _stream(stream))
+    B, hk, hv, dk, dv = d.batch, d.h_k, d.h_v, d.d_k, d.d_v
+    io, n = _io_dtype(d), state.shape[0]
+    rc = _lib.gdn_rule_step(
+        d, None if slot is None else _ints(slot, (B,), "slot"), n, _attn_rows(q, B, hk, dk, io, "q"),
+        _attn_rows(k, B, hk, dk, io, "k"), _attn_rows(v, B, hv, dv, io, "v"), _f32s(beta, (B, hv), "beta"),
+        _f32s(g, (B, hv), "g"), _f32s(state, (n, hv, dv, dk), "state"), _attn_rows(o, B, hv, dv, io, "o"),
+        _stream(stream))
+    if rc:
+        raise GdnError(rc, "gdn_rule_step")
 
 
 # ---------------------------------------------------------------- scores of tokens
@@ -844,30 +868,43 @@ def _logits(x, d, name):
     return x.data_ptr()
 
 
-def _floats(x, shape, name):
-    return _ptr(x, shape, torch.float32, name)
+@functools.lru_cache(maxsize=None)
+def _score_bytes_of(*sizes):
+    return gdn_score_workspace_bytes(ScoreDims(*sizes))
+
+
+def _tokens(x, shape, name):
+    return None if x is None else _ints(x, shape, name)
 
 
 def gdn_token_scores(d: ScoreDims, logits, tokens, logp, entropy, lse, workspace, top_logp=None, top_tok=None,
                      stream=None) -> None:
     """Enqueue the scores of every row (see gdn_score.h).  tokens with logp, entropy, lse: None where not
     wanted; top_logp and top_tok: [rows, topk]."""
-    n, k, need = (d.rows,), (d.rows, d.topk), gdn_score_workspace_bytes(d)
-    if workspace.dtype != torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous() or \
-            workspace.numel() < need:
+    rows, topk = d.rows, d.topk
+    n, k = (rows,), (rows, topk)
+    need = _score_bytes_of(rows, d.row_stride, d.vocab, topk, d.io_dtype)
+    if workspace.dtype is not torch.uint8 or workspace.numel() < need or not workspace.is_cuda or \
+            not workspace.is_contiguous():
         raise ValueError(f"workspace: expected {need} contiguous bytes or more (score_workspace)")
-    _call("gdn_token_scores", ctypes.byref(d), _logits(logits, d, "logits"), _ptr(tokens, n, _int32, "tokens"),
-          _floats(logp, n, "logp"), _floats(entropy, n, "entropy"), _floats(lse, n, "lse"),
-          _floats(top_logp, k, "top_logp"), _ptr(top_tok, k, _int32, "top_tok"), workspace.data_ptr(),
-          _stream(stream))
+    rc = _lib.gdn_token_scores(
+        d, _logits(logits, d, "logits"), _tokens(tokens, n, "tokens"), _f32s(logp, n, "logp"),
+        _f32s(entropy, n, "entropy"), _f32s(lse, n, "lse"), _f32s(top_logp, k, "top_logp"),
+        _tokens(top_tok, k, "top_tok"), workspace.data_ptr(), _stream(stream))
+    if rc:
+        raise GdnError(rc, "gdn_token_scores")
 
 
 def gdn_token_scores_backward(d: ScoreDims, logits, tokens, lse, entropy, d_logp, d_entropy, d_logits, top_tok=None,
                               d_top_logp=None, stream=None) -> None:
     """Enqueue the gradient of the logits (see gdn_score.h).  d_logp, d_entropy, d_top_logp: None where there is
     none; d_logits may be logits."""
-    n, k = (d.rows,), (d.rows, d.topk)
-    _call("gdn_token_scores_backward", ctypes.byref(d), _logits(logits, d, "logits"),
-          _ptr(tokens, n, _int32, "tokens"), _floats(lse, n, "lse"), _floats(entropy, n, "entropy"),
-          _floats(d_logp, n, "d_logp"), _floats(d_entropy, n, "d_entropy"), _ptr(top_tok, k, _int32, "top_tok"),
-          _floats(d_top_logp, k, "d_top_logp"), _logits(d_logits, d, "d_logits"), _stream(stream))
+    rows = d.rows
+    n, k = (rows,), (rows, d.topk)
+    rc = _lib.gdn_token_scores_backward(
+        d, _logits(logits, d, "logits"), _tokens(tokens, n, "tokens"), _f32s(lse, n, "lse"),
+        _f32s(entropy, n, "entropy"), _f32s(d_logp, n, "d_logp"), _f32s(d_entropy, n, "d_entropy"),
+        _tokens(top_tok, k, "top_tok"), _f32s(d_top_logp, k, "d_top_logp"), _logits(d_logits, d, "d_logits"),
+        _stream(stream))
+    if rc:
+        raise GdnError(rc, "gdn_token_scores_backward")
