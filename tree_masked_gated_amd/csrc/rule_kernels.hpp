@@ -223,6 +223,14 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
     }
 }
 
+// A [row][column] tile of 16 columns in LDS, as operands of 32-row contraction steps: step k holds
+// lane l's eight rows 32 k + 8 (l / 16) .. of column l % 16 at l * 8.  place4: rows row .. row + 3, row a
+// multiple of 4, of a tile that begins with step `first`.
+constexpr int kStep = 64 * 8;
+__device__ __forceinline__ int place4(int first, int row, int n) {
+    return ((first + (row >> 5)) * 64 + n + 16 * ((row >> 3) & 3)) * 8 + (row & 4);
+}
+
 // ------------------------------------------------------------------ scan
 //
 // One workgroup per (sequence, value head, slice of 16 NC value columns).  d_k / 32 state waves:
@@ -230,9 +238,9 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
 // phases with a barrier between them: every wave's H goes to LDS as operand terms; row tile i (16
 // rows) of K H, then of W, is formed by wave i, which needs all of the one before; H' needs all of
 // U.  The outputs are formed by waves of their own, from the terms of H and U that the state waves
-// leave in LDS, in the time that those take for the next step.  Terms lie in LDS as
-// [column][row], where accumulators have four rows to a lane (8-byte writes) and operands eight
-// (16-byte reads).  (Parts of K H from each wave's own rows of H, added up in LDS, took 1.1 times as
+// leave in LDS, in the time that those take for the next step.  Terms lie in LDS as operands are
+// read, 16 bytes to a lane (rows padded to spread over the banks took twice the reads' time);
+// accumulators have four rows to a lane, 8 bytes of that.  (Parts of K H from each wave's own rows of H, added up in LDS, took 1.1 times as
 // long: 16-byte LDS writes take 20 to 40 cycles each where reads take 9.)
 //
 // A single sequence's scan is bound by what one state wave issues per chunk, one after the other,
@@ -377,7 +385,7 @@ struct Outputs {
             for (int s = 0; s < 2; ++s) {
                 if (s > tile[ii] / 2) continue;
                 bf16x8 ub[R];
-                get8<R>(u + 32 * s + 8 * q4, plane, ub);
+                get8<R>(u + s * kStep + lane * 8, plane, ub);
                 y = mma<R, R>(ym[ii][s], ub, y);
             }
 #pragma unroll
@@ -404,10 +412,8 @@ rule_scan(const RuleArgs a) {
     constexpr int NI = D::NI, NX = D::NX;
     constexpr bool kHold = DK * P <= 256;            // K and Q are held in registers, or read as they are used
     constexpr int KH = kHold ? KS : 1;
-    constexpr int LH = DK + 8;
-    constexpr int kPl = NC * 16 * kTp, kPh = NC * 16 * LH; // elements of a plane of a [column][row] tile
-    __shared__ __attribute__((aligned(16))) uint16_t hh[S][NC * 16][LH], rr[S][NC * 16][kTp], uu[R][NC * 16][kTp],
-        ue[S][NC * 16][kTp];
+    constexpr int kPl = NC * 2 * kStep, kPh = NC * KS * kStep; // elements of a term of a tile
+    __shared__ __attribute__((aligned(16))) uint16_t hh[S * kPh], rr[S * kPl], uu[R * kPl], ue[S * kPl];
 
     int b, hv, sl;
     scan_place<IO, DK>(a, a.dvp / (16 * NC), b, hv, sl);
@@ -448,7 +454,7 @@ rule_scan(const RuleArgs a) {
 #pragma unroll
                 for (int cc = 0; cc < NC; ++cc) {
                     bf16x8 hb[R];
-                    get8<R>(&hh[0][16 * cc + n][32 * s + 8 * q4], kPh, hb);
+                    get8<R>(hh + (cc * KS + s) * kStep + lane * 8, kPh, hb);
                     out.add(s, cc, hb);
                 }
             }
@@ -458,7 +464,7 @@ rule_scan(const RuleArgs a) {
             lds_barrier();
 #pragma unroll
             for (int cc = 0; cc < NC; ++cc)
-                out.finish(cc, &uu[0][16 * cc + n][0], kPl, po + 16 * cc * E, more ? kC : tail, col0 + 16 * cc < a.dv, lane);
+                out.finish(cc, uu + 2 * cc * kStep, kPl, po + 16 * cc * E, more ? kC : tail, col0 + 16 * cc < a.dv, lane);
             po += o_step;
             out.py += more ? y_step : 0;
             out.pc += more ? co_step : 0;
@@ -568,7 +574,7 @@ rule_scan(const RuleArgs a) {
         for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                put4<S>(&hh[0][16 * cc + n][32 * wv + 16 * t + 4 * q4], kPh, h[t][cc]);
+                put4<S>(hh + place4(cc * KS, 32 * wv + 16 * t + 4 * q4, n), kPh, h[t][cc]);
                 if constexpr (BACK)                  // the state before the chunk, for the gradients
 #pragma unroll
                     for (int r = 0; r < 4; ++r) ph[(16 * t + r) * a.dvp + 16 * cc] = h[t][cc][r];
@@ -590,7 +596,7 @@ rule_scan(const RuleArgs a) {
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 bf16x8 hb[S];
-                get8<S>(&hh[0][16 * deal.block(x) + n][32 * s + 8 * q4], kPh, hb);
+                get8<S>(hh + (deal.block(x) * KS + s) * kStep + lane * 8, kPh, hb);
 #pragma unroll
                 for (int ii = 0; ii < NI; ++ii) f[ii][x] = mma<P, S>(kf[ii][kHold ? s : 0], hb, f[ii][x]);
                 if constexpr (OUT == kOutSame) out.add(s, x, hb);
@@ -601,7 +607,7 @@ rule_scan(const RuleArgs a) {
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 f[ii][x] = v[ii][x].get(rows) - ca[ii] * f[ii][x];
-                put4<S>(&rr[0][16 * deal.block(x) + n][16 * deal.tile(ii) + 4 * q4], kPl, cb[ii] * f[ii][x]);
+                put4<S>(rr + place4(2 * deal.block(x), 16 * deal.tile(ii) + 4 * q4, n), kPl, cb[ii] * f[ii][x]);
             }
         pk += more ? key_step : 0;
         pca += more ? co_step : 0;
@@ -623,16 +629,16 @@ rule_scan(const RuleArgs a) {
                 for (int s = 0; s < 2; ++s) {
                     if (s > i / 2) continue;
                     bf16x8 r[S];
-                    get8<S>(&rr[0][16 * cc + n][32 * s + 8 * q4], kPl, r);
+                    get8<S>(rr + (2 * cc + s) * kStep + lane * 8, kPl, r);
                     m = mma<S, S>(tm[ii][s], r, m);
                 }
                 const f32x4 w = f[ii][x] - m, u = cb[ii] * w;
-                put4<S>(&ue[0][16 * cc + n][16 * i + 4 * q4], kPl, ce[ii] * u);
+                put4<S>(ue + place4(2 * cc, 16 * i + 4 * q4, n), kPl, ce[ii] * u);
                 if constexpr (BACK) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) pw[(16 * i + r) * a.dvp + 16 * cc] = w[r];
                 } else {
-                    put4<R>(&uu[0][16 * cc + n][16 * i + 4 * q4], kPl, u);
+                    put4<R>(uu + place4(2 * cc, 16 * i + 4 * q4, n), kPl, u);
                 }
             }
         }
@@ -645,7 +651,7 @@ rule_scan(const RuleArgs a) {
         for (int cc = 0; cc < NC; ++cc) {
             bf16x8 u[2][S];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) get8<S>(&ue[0][16 * cc + n][32 * s + 8 * q4], kPl, u[s]);
+            for (int s = 0; s < 2; ++s) get8<S>(ue + (2 * cc + s) * kStep + lane * 8, kPl, u[s]);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 h[t][cc] = end * h[t][cc];
@@ -660,7 +666,7 @@ rule_scan(const RuleArgs a) {
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 const int cc = deal.block(x);
-                out.finish(x, &uu[0][16 * cc + n][0], kPl, po + 16 * cc * E, rows, col0 + 16 * cc < a.dv, lane);
+                out.finish(x, uu + 2 * cc * kStep, kPl, po + 16 * cc * E, rows, col0 + 16 * cc < a.dv, lane);
             }
             po += o_step;
             out.py += more ? y_step : 0;
@@ -735,10 +741,9 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
     typedef Deal<NW, NC> D;
     constexpr int NI = D::NI, NX = D::NX;
     constexpr bool kHold = DK * P <= 256;
-    constexpr int KH = kHold ? KS : 1, LH = DK + 8;
-    constexpr int kPl = NC * 16 * kTp, kPh = NC * 16 * LH; // elements of a plane of a [column][row] tile
-    __shared__ __attribute__((aligned(16))) uint16_t hh[S][NC * 16][LH], od[P][NC * 16][kTp], oa[S][NC * 16][kTp],
-        ou[S][NC * 16][kTp], oz[S][NC * 16][kTp];
+    constexpr int KH = kHold ? KS : 1;
+    constexpr int kPl = NC * 2 * kStep, kPh = NC * KS * kStep; // elements of a term of a tile
+    __shared__ __attribute__((aligned(16))) uint16_t hh[S * kPh], od[P * kPl], oa[S * kPl], ou[S * kPl], oz[S * kPl];
 
     int b, hv, sl;
     const int slices = a.dvp / (16 * NC);
@@ -873,14 +878,14 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
             for (int x = 0; x < NX; ++x) {
                 const int i = deal.tile(ii), cc = deal.block(x);
                 d_o[ii][x] = raw[ii][x].get(seq.n - c * kC);
-                put4<P>(&od[0][16 * cc + n][16 * i + 4 * q4], kPl, d_o[ii][x]);
+                put4<P>(od + place4(2 * cc, 16 * i + 4 * q4, n), kPl, d_o[ii][x]);
             }
         float pa = 0.f;
 #pragma unroll
         for (int cc = 0; cc < NC; ++cc)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                put4<S>(&hh[0][16 * cc + n][32 * wv + 16 * t + 4 * q4], kPh, dh[t][cc]);
+                put4<S>(hh + place4(cc * KS, 32 * wv + 16 * t + 4 * q4, n), kPh, dh[t][cc]);
                 float* to = a.dht + (val * DK + 32 * wv + 16 * t + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -905,7 +910,7 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 bf16x8 hb[S];
-                get8<S>(&hh[0][16 * deal.block(x) + n][32 * s + 8 * q4], kPh, hb);
+                get8<S>(hh + (deal.block(x) * KS + s) * kStep + lane * 8, kPh, hb);
 #pragma unroll
                 for (int ii = 0; ii < NI; ++ii) du[ii][x] = mma<P, S>(kf[ii][kHold ? s : 0], hb, du[ii][x]);
             }
@@ -923,12 +928,12 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
                 for (int st = 0; st < 2; ++st) {
                     if (st < i / 2) continue;
                     bf16x8 d[P];
-                    get8<P>(&od[0][16 * cc + n][32 * st + 8 * q4], kPl, d);
+                    get8<P>(od + (2 * cc + st) * kStep + lane * 8, kPl, d);
                     s = mma<S, P>(yt[ii][st], d, s);
                 }
                 du[ii][x] = s;
-                put4<S>(&ou[0][16 * cc + n][16 * i + 4 * q4], kPl, cb[ii] * s);
-                put4<S>(&oa[0][16 * cc + n][16 * i + 4 * q4], kPl, ca[ii] * d_o[ii][x]);
+                put4<S>(ou + place4(2 * cc, 16 * i + 4 * q4, n), kPl, cb[ii] * s);
+                put4<S>(oa + place4(2 * cc, 16 * i + 4 * q4, n), kPl, ca[ii] * d_o[ii][x]);
             }
         }
         load_b(next);
@@ -946,11 +951,11 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
                 for (int s = 0; s < 2; ++s) {
                     if (s < i / 2) continue;
                     bf16x8 u[S];
-                    get8<S>(&ou[0][16 * cc + n][32 * s + 8 * q4], kPl, u);
+                    get8<S>(ou + (2 * cc + s) * kStep + lane * 8, kPl, u);
                     m = mma<S, S>(tt[ii][s], u, m);
                 }
                 const f32x4 dr = du[ii][x] - m, dv = cb[ii] * dr;
-                put4<S>(&oz[0][16 * cc + n][16 * i + 4 * q4], kPl, -ca[ii] * dv);
+                put4<S>(oz + place4(2 * cc, 16 * i + 4 * q4, n), kPl, -ca[ii] * dv);
                 float* to = a.dr + (val * kC + 16 * i + 4 * q4) * a.dvp + col0 + 16 * cc;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
@@ -978,8 +983,8 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
             bf16x8 u[2][S], z[2][S];
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                get8<S>(&oa[0][16 * cc + n][32 * s + 8 * q4], kPl, u[s]);
-                get8<S>(&oz[0][16 * cc + n][32 * s + 8 * q4], kPl, z[s]);
+                get8<S>(oa + (2 * cc + s) * kStep + lane * 8, kPl, u[s]);
+                get8<S>(oz + (2 * cc + s) * kStep + lane * 8, kPl, z[s]);
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
