@@ -112,6 +112,37 @@ def test_forward_and_backward(sizes, hk, hv, dk, dv, io):
     check(x, {**forward(x), **backward(x)}, io)
 
 
+# Batches of many sequences, most of them empty or short, for which the scans take wider slices; with no more
+# than 64 sequences the longest go first.
+MANY = [(60, 4, 8, 64, 80), (70, 2, 4, 128, 128), (60, 4, 12, 100, 33), (20, 4, 8, 128, 128), (36, 2, 4, 48, 128),
+        (20, 2, 4, 200, 96)]
+
+
+def many(batch, *heads, io):
+    sizes = [3, 0, 130, 1, 64, 65, 0, 200, 63, 2] + [i % 3 for i in range(batch - 10)]
+    return make(sizes, *heads, io)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("batch,hk,hv,dk,dv", MANY)
+def test_many_sequences(batch, hk, hv, dk, dv, io):
+    x = many(batch, hk, hv, dk, dv, io=io)
+    check(x, {**forward(x), **backward(x)}, io)
+
+
+@pytest.mark.parametrize("batch,dv", [(2, 128), (20, 128), (70, 128), (70, 33)])
+def test_outputs_in_a_wider_tensor(batch, dv):
+    """Outputs at odd places between others, which stay as they were."""
+    x = many(batch, 2, 4, 128, dv, io="bf16") if batch > 9 else make([67, 130], 2, 4, 128, dv, "bf16")
+    want, n = forward(x)["o"], x["v"].shape[0]
+    wide = torch.full((n, 4, dv + 9), 7.0, dtype=torch.bfloat16, device="cuda")
+    for at in (1, 4, 8):
+        wide.fill_(7)
+        forward(x, o=wide[:, :, at:at + dv])
+        assert torch.equal(wide[:, :, at:at + dv], want)
+        assert (wide[:, :, :at] == 7).all() and (wide[:, :, at + dv:] == 7).all()
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_without_states(io):
     """No state before, none asked for; dS_out and dS0 neither."""

@@ -179,7 +179,7 @@ int gdn_rule_forward(const gdn_rule_dims* dims, const int32_t* offsets, int64_t 
     a.offsets = offsets;
     if (n_rows > 0) {
         a.q = rows_of(q), a.k = rows_of(k), a.v = rows_of(v), a.o = rows_of(o);
-        a.vq = vectors(q, a.dk, io), a.vk = vectors(k, a.dk, io);
+        a.vq = vectors(q, a.dk, io), a.vk = vectors(k, a.dk, io), a.vo = vectors(o, 8, io);
     }
     a.beta = beta, a.g = g, a.S0 = S0, a.S_out = S_out;
     const int dkp = padded_dk(dims);

@@ -247,6 +247,23 @@ __device__ __forceinline__ int place4(int first, int row, int n) {
 // so addresses are kept as running pointers, and operands of a chunk are requested while the chunk
 // before it is worked on.
 // BACK: instead of the outputs, the state before each chunk and W are kept for the gradients.
+// The place-th longest sequence, where there are more workgroups than places for them: those that
+// take longest begin first, so that none begins when the rest are nearly done.  A wave orders up to
+// 64 sequences by itself; with more, what a place gets averages out.  (24 prompts of 0 to 2048 rows,
+// 32 heads: 553 us in the order of the batch, 480 longest first.)
+constexpr int kPlaces = 512;                         // two workgroups to a compute unit
+__device__ __forceinline__ int longest(const RuleArgs& a, int place) {
+    if (gridDim.x <= kPlaces || a.B > 64) return place;
+    const int lane = threadIdx.x & 63;
+    const int n = lane < a.B ? rule_seq(a, lane).n : -1;
+    int before = 0;
+    for (int j = 0; j < a.B; ++j) {
+        const int other = __builtin_amdgcn_readlane(n, j);
+        before += other > n || (other == n && j < lane);
+    }
+    return __ffsll((unsigned long long)__ballot(lane < a.B && before == place)) - 1;
+}
+
 template <int IO, int DK>
 __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b, int& hv, int& sl) {
     // Workgroups go to the eight XCDs in turn: the slices of a head stay on one, whose L2 they share.
@@ -262,6 +279,7 @@ __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b
     }
     b = head / a.Hv;
     hv = head - b * a.Hv;
+    b = longest(a, b);
 }
 
 // Elements of value rows, four rows 16 i + 4 q4 + r of a chunk in one column: requested a chunk
@@ -689,6 +707,273 @@ rule_scan(const RuleArgs a) {
                     if (i < a.dk && j < a.dv) a.S_out[state + (size_t)j * a.dk + i] = h[t][cc][r];
                 }
     }
+}
+
+// ------------------------------------------------------------------ scan, wide
+//
+// The scan for many slices: a workgroup of four waves takes 64 value columns of a head, and a wave 16
+// of them with all of H (d_k rows), so that nothing of a chunk passes between waves: accumulators
+// become operands by swaps of lanes.  What the waves share are the chunk's operands, which come to
+// LDS once for all four, past the registers.  Each of the three parts of a chunk (K and Q; M;
+// K^T and Y) has its place there; the next chunk's part is sent for when every wave is done with it, and
+// waited for where two parts of work have passed since.  bf16 rows only: three terms of every
+// operand would not fit.  Outputs are formed transposed, so that a lane has four columns of a row.
+//
+// 81 KB of LDS: two workgroups to a compute unit.  24 prompts, 26490 rows, 32 heads: 480 us, 16 K
+// cycles a chunk for the two waves of a SIMD, whose matrix instructions are 5.8 K; between them stand
+// the terms of H and the waits at the chunk's three barriers.  (rule_scan with two column blocks and
+// the outputs by the state's waves: 555 us; every operand read just before its use: 570 us.)
+constexpr int kWide = 64;
+
+// 16 bytes a lane from memory to LDS.  from and to are the wave's; at: the lane's place from there.
+__device__ __forceinline__ void send16(const char* from, uint32_t to, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(to), "v"(at), "s"(from) : "memory");
+}
+template <class X>
+__device__ __forceinline__ uint32_t lds_at(X& x) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) X*)&x;
+}
+// Fragments to LDS, dealt to the waves; `to` and `from` the same for the workgroup.  A wave past the
+// last fragment sends that one again, to the same place.
+template <int N>
+__device__ __forceinline__ void send(const char* from, uint32_t to, int wv, int lane) {
+#pragma unroll
+    for (int x = 0; x < (N + 3) / 4; ++x) {
+        const int f = N % 4 ? min(wv + 4 * x, N - 1) : wv + 4 * x;
+        send16(from + f * kFrag, to + f * kFrag, lane * 16);
+    }
+}
+
+// Tiles 2 s and 2 s + 1 of a column of accumulators, as the terms of one contraction step.
+template <int T>
+__device__ __forceinline__ void operand(f32x4 x, f32x4 y, bf16x8 (&to)[T]) {
+    s16x4 a[T], b[T];
+    split4p(x, a);
+    split4p(y, b);
+#pragma unroll
+    for (int p = 0; p < T; ++p) to[p] = stack_pair(a[p], b[p]);
+}
+
+// Nothing is moved past this: operands that are read before it are on their way during what follows,
+// where the compiler would read each just before its use and wait for it.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
+
+template <int DK>
+__global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
+    constexpr int IO = GDN_BF16, KS = DK / 32, NT = DK / 16, S = kSum, R = kRound<IO>;
+    constexpr int nK = 4 * KS, nM = kTriFrags * S, nT = 2 * NT, nY = kTriFrags * R;
+    __shared__ __attribute__((aligned(16))) char sk[nK * kFrag], sq[nK * kFrag], sm[nM * kFrag], st[nT * kFrag],
+        sy[nY * kFrag];
+    __shared__ float sc[2][3 * kC];
+
+    int b, hv, sl;
+    scan_place<IO, DK>(a, (a.dvp + kWide - 1) / kWide, b, hv, sl);
+    const int hk = hv / a.group;
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q4 = lane >> 4;
+    const RuleSeq seq = rule_seq(a, b);
+    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
+    const int tail = seq.n - (chunks - 1) * kC;
+    const int block = sl * kWide + 16 * wv, col = block + n; // the wave's columns; this lane's
+    const bool work = block < a.dvp;                 // columns past d_v have zeros to work on, past dvp no place
+    const size_t key = ((size_t)base * a.Hk + hk) * nK * kFrag, val = (size_t)base * a.Hv + hv;
+    const size_t key_step = (size_t)a.Hk * nK * kFrag, m_step = (size_t)a.Hv * nM * kFrag, y_step = (size_t)a.Hv * nY * kFrag;
+    const size_t co_step = (size_t)a.Hv * 3 * kC;
+
+    f32x4 h[NT];                                     // rows 16 t + 4 q4 + r
+    const size_t state = ((size_t)b * a.Hv + hv) * a.dv * a.dk + (size_t)min(col, a.dv - 1) * a.dk;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * t + 4 * q4 + r;
+            h[t][r] = a.S0 && i < a.dk && col < a.dv ? a.S0[state + i] : 0.f;
+        }
+    const char *pk = a.kf + key, *pq = a.qf + key, *pt = a.kt + key, *pm = a.tm + val * nM * kFrag, *py = a.ym + val * nY * kFrag;
+    const float* pc = a.coef + val * 3 * kC;
+    uint16_t v[4][4];                                // of the next chunk: rows 16 i + 4 q4 + r
+    const uint16_t* pv = reinterpret_cast<const uint16_t*>(a.v.p) + (seq.row0 + 4 * q4) * a.v.row + hv * a.v.head + min(col, a.dv - 1);
+    uint16_t* po = reinterpret_cast<uint16_t*>(a.o.p) + (seq.row0 + n) * a.o.row + hv * a.o.head + block + 4 * q4;
+    // the coefficients of chunk c: every lane of the first wave's three quarters sends 16 bytes
+    auto send_coef = [&](int c) {
+        if (wv == 0 && lane < 3 * kC / 4) send16((const char*)pc, lds_at(sc) + (c & 1) * sizeof(sc[0]), lane * 16);
+    };
+    auto send_k = [&] {
+        send<nK>(pk, lds_at(sk), wv, lane);
+        send<nK>(pq, lds_at(sq), wv, lane);
+    };
+    auto send_t = [&] {
+        send<nT>(pt, lds_at(st), wv, lane);
+        send<nY>(py, lds_at(sy), wv, lane);
+    };
+    auto load_v = [&](int rows) {
+        if (rows == kC) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[i][r] = pv[(16 * i + r) * a.v.row];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[i][r] = pv[(min(16 * i + 4 * q4 + r, rows - 1) - 4 * q4) * a.v.row];
+        }
+    };
+    if (chunks > 0) {
+        send_k();
+        send_coef(0);
+        load_v(chunks > 1 ? kC : tail);
+        send<nM>(pm, lds_at(sm), wv, lane);
+    }
+    wait_vmem_all();
+    for (int c = 0; c < chunks; ++c) {
+        const bool more = c + 1 < chunks;
+        const int rows = more ? kC : tail;
+        const float* co = sc[c & 1];
+        lds_barrier();                               // K, Q and M are here, K^T and Y free
+        send_t();
+        f32x4 f[4], o[4];
+        bf16x8 rb[2][S];
+        if (work) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = o[i] = f32x4{0, 0, 0, 0};
+            bf16x8 k[4][1], q[4][1];
+            auto read = [&](const char* from, int s, bf16x8 (&x)[4][1]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i][0] = load_frag(from + (i * KS + s) * kFrag, lane);
+            };
+            read(sk, 0, k);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                read(sq, s, q);
+                hold();
+                bf16x8 hb[S];
+                operand(h[2 * s], h[2 * s + 1], hb);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = mma<1, S>(k[i], hb, f[i]);
+                hold();
+                if (s + 1 < KS) read(sk, s + 1, k);
+                hold();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] = mma<R, 1>(hb, q[i], o[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 ca = *reinterpret_cast<const f32x4*>(co + 16 * i + 4 * q4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    f[i][r] = (16 * i + 4 * q4 + r < rows && col < a.dv ? bf16_bits_to_f32(v[i][r]) : 0.f) - ca[r] * f[i][r];
+                o[i] = co[16 * i + n] * o[i];
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 b0 = *reinterpret_cast<const f32x4*>(co + 2 * kC + 32 * s + 4 * q4);
+                const f32x4 b1 = *reinterpret_cast<const f32x4*>(co + 2 * kC + 32 * s + 16 + 4 * q4);
+                operand(b0 * f[2 * s], b1 * f[2 * s + 1], rb[s]);
+            }
+        }
+        wait_vmem_all();                             // K^T and Y
+        lds_barrier();                               // K and Q are free
+        pk += more ? key_step : 0;
+        pq += more ? key_step : 0;
+        pc += more ? co_step : 0;
+        send_k();
+        send_coef(c + 1);
+        pv += more ? kC * a.v.row : 0;
+        load_v(c + 2 < chunks ? kC : tail);
+        bf16x8 ub[2][S], uy[2][R];
+        if (work) {
+            f32x4 u[4];
+            bf16x8 x[2][2][S];
+            auto read = [&](int i) {
+#pragma unroll
+                for (int s = 0; s <= i / 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < S; ++p) x[i & 1][s][p] = load_frag(sm + (low_frag(i, s) * S + p) * kFrag, lane);
+            };
+            read(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < 3) read(i + 1);
+                hold();
+                f32x4 m = {0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s <= i / 2; ++s) m = mma<S, S>(x[i & 1][s], rb[s], m);
+                const f32x4 w = f[i] - m;
+                u[i] = *reinterpret_cast<const f32x4*>(co + 2 * kC + 16 * i + 4 * q4) * w;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 e0 = *reinterpret_cast<const f32x4*>(co + kC + 32 * s + 4 * q4);
+                const f32x4 e1 = *reinterpret_cast<const f32x4*>(co + kC + 32 * s + 16 + 4 * q4);
+                operand(e0 * u[2 * s], e1 * u[2 * s + 1], ub[s]);
+                operand(u[2 * s], u[2 * s + 1], uy[s]);
+            }
+        }
+        lds_barrier();                               // M is free
+        pm += more ? m_step : 0;
+        send<nM>(pm, lds_at(sm), wv, lane);
+        if (work) {
+            const float end = co[kC - 1];
+            bf16x8 k[2][2][2][1];                    // of two tiles, and of the next two
+            auto read = [&](int t) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) k[t / 2 & 1][x / 2][x % 2][0] = load_frag(st + (2 * t + x) * kFrag, lane);
+            };
+            bf16x8 y[2][2][R];
+            auto read_y = [&](int i) {
+#pragma unroll
+                for (int s = 0; s <= i / 2; ++s)
+#pragma unroll
+                    for (int p = 0; p < R; ++p) y[i & 1][s][p] = load_frag(sy + (low_frag(i, s) * R + p) * kFrag, lane);
+            };
+            read(0);
+#pragma unroll
+            for (int t = 0; t < NT; t += 2) {
+                if (t + 2 < NT) read(t + 2);
+                else read_y(0);
+                hold();
+#pragma unroll
+                for (int x = 0; x < 2; ++x) h[t + x] = end * h[t + x];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) h[t + x] = mma<1, S>(k[t / 2 & 1][x][s], ub[s], h[t + x]);
+            }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (i < 3) read_y(i + 1);
+                    hold();
+#pragma unroll
+                    for (int s = 0; s <= i / 2; ++s) o[i] = mma<R, R>(uy[s], y[i & 1][s], o[i]);
+                }
+        }
+        pt += more ? key_step : 0;
+        py += more ? y_step : 0;
+        wait_vmem_all();                             // K, Q, M, V and the coefficients
+        if (work) {
+            // o[i]: row 16 i + n, columns block + 4 q4 + r
+            if (a.vo && rows == kC && block + 16 <= a.dv) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) *reinterpret_cast<s16x4*>(po + 16 * i * a.o.row) = to_bf16x4(o[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * i + n < rows && block + 4 * q4 + r < a.dv) po[16 * i * a.o.row + r] = bf16_rne(o[i][r]);
+            }
+        }
+        po += kC * a.o.row;
+    }
+    if (a.S_out && col < a.dv)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * t + 4 * q4 + r;
+                if (i < a.dk) a.S_out[state + i] = h[t][r];
+            }
 }
 
 // ------------------------------------------------------------------ scan_back
@@ -1329,17 +1614,26 @@ __global__ void __launch_bounds__(64) rule_gates(const RuleArgs a, int parts, in
 // Workgroups of a scan with slices of 16 value columns.
 inline int64_t slices_of_16(const RuleArgs& a) { return (int64_t)a.B * a.Hv * (a.dvp / 16); }
 
+template <int DK>
+hipError_t scan_wide_launch(const RuleArgs& a, hipStream_t stream) {
+    return launch(rule_scan_wide<DK>, dim3(a.B * a.Hv * ((a.dvp + kWide - 1) / kWide)), dim3(256), 0, stream, a);
+}
+
 template <int IO, int DK, int NC, int OUT>
 hipError_t scan_launch(const RuleArgs& a, hipStream_t stream) {
     const int waves = DK / 32 + (OUT == kOutOwn ? kOutWaves<DK> : 0);
     return launch(rule_scan<IO, DK, NC, OUT>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))), dim3(waves * 64), 0, stream, a);
 }
 
-// Few slices, no more than two to a compute unit: the narrowest ones, and waves of their own for the
-// outputs (one sequence of 8192 rows, 32 heads, 256 slices: 251 us against 357).  Many: two column
-// blocks to a workgroup, which then reads half as many operands per column, and no waves but the
-// state's, so that two workgroups share a unit (24 prompts, 26490 rows, 6144 slices: 582 us against 863).
-constexpr int64_t kFewSlices = 512;
+// Which scan, by the number of slices of 16 columns (d_k 128, bf16; us for uneven lengths up to 2048):
+//   slices                    512    768   1024   2048   4096
+//   outputs by own waves       86     81    138    242    308   narrowest, shortest chunk of all
+//   two column blocks          91     91    120    170    187   half the operands read per column
+//   wide                      148    144    146    196    168   a quarter, longest chunk of all
+// Waves of their own for the outputs while the workgroups have places: a workgroup of d_k 64 has half
+// the waves.  The wide one where it has more workgroups than places.
+template <int DK>
+constexpr int64_t kFewSlices = kPlaces * 128 / DK;
 template <int IO, int DK>
 hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
     hipError_t e = hipSuccess;
@@ -1349,8 +1643,10 @@ hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
     if constexpr (DK == 256) {
         return scan_launch<IO, DK, 2, kOutSame>(a, stream);
     } else {
-        return slices_of_16(a) <= kFewSlices ? scan_launch<IO, DK, 1, kOutOwn>(a, stream)
-                                      : scan_launch<IO, DK, 2, kOutSame>(a, stream);
+        if (slices_of_16(a) <= kFewSlices<DK>) return scan_launch<IO, DK, 1, kOutOwn>(a, stream);
+        if constexpr (IO == GDN_BF16)
+            if (slices_of_16(a) > 4 * kPlaces) return scan_wide_launch<DK>(a, stream);
+        return scan_launch<IO, DK, 2, kOutSame>(a, stream);
     }
 }
 
@@ -1379,7 +1675,7 @@ hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
     if constexpr (DK == 256)
         return back_launch<IO, DK, 2>(a, stream);
     else
-        return slices_of_16(a) <= kFewSlices ? back_launch<IO, DK, 1>(a, stream) : back_launch<IO, DK, 2>(a, stream);
+        return slices_of_16(a) <= kPlaces ? back_launch<IO, DK, 1>(a, stream) : back_launch<IO, DK, 2>(a, stream);
 }
 
 }  // namespace gdn
