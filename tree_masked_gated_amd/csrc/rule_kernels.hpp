@@ -231,22 +231,10 @@ __device__ __forceinline__ int place4(int first, int row, int n) {
     return ((first + (row >> 5)) * 64 + n + 16 * ((row >> 3) & 3)) * 8 + (row & 4);
 }
 
-// ------------------------------------------------------------------ scan
-//
-// One workgroup per (sequence, value head, slice of 16 NC value columns).  d_k / 32 state waves:
-// wave w keeps rows 32 w .. 32 w + 31 of the slice of H in accumulators (fp32).  A chunk goes in four
-// phases with a barrier between them: every wave's H goes to LDS as operand terms; row tile i (16
-// rows) of K H, then of W, is formed by wave i, which needs all of the one before; H' needs all of
-// U.  The outputs are formed by waves of their own, from the terms of H and U that the state waves
-// leave in LDS, in the time that those take for the next step.  Terms lie in LDS as operands are
-// read, 16 bytes to a lane (rows padded to spread over the banks took twice the reads' time);
-// accumulators have four rows to a lane, 8 bytes of that.  (Parts of K H from each wave's own rows of H, added up in LDS, took 1.1 times as
-// long: 16-byte LDS writes take 20 to 40 cycles each where reads take 9.)
-//
-// A single sequence's scan is bound by what one state wave issues per chunk, one after the other,
-// so addresses are kept as running pointers, and operands of a chunk are requested while the chunk
-// before it is worked on.
-// BACK: instead of the outputs, the state before each chunk and W are kept for the gradients.
+// Nothing is moved past this: operands that are read before it are on their way during what follows,
+// where the compiler would read each just before its use and wait for it.
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
+
 // The place-th longest sequence, where there are more workgroups than places for them: those that
 // take longest begin first, so that none begins when the rest are nearly done.  A wave orders up to
 // 64 sequences by itself; with more, what a place gets averages out.  (24 prompts of 0 to 2048 rows,
@@ -261,7 +249,7 @@ __device__ __forceinline__ int longest(const RuleArgs& a, int place) {
         const int other = __builtin_amdgcn_readlane(n, j);
         before += other > n || (other == n && j < lane);
     }
-    return __ffsll((unsigned long long)__ballot(lane < a.B && before == place)) - 1;
+    return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)__ballot(lane < a.B && before == place)) - 1);
 }
 
 template <int IO, int DK>
@@ -281,6 +269,7 @@ __device__ __forceinline__ void scan_place(const RuleArgs& a, int slices, int& b
     hv = head - b * a.Hv;
     b = longest(a, b);
 }
+
 
 // Elements of value rows, four rows 16 i + 4 q4 + r of a chunk in one column: requested a chunk
 // ahead as they lie in memory, converted and masked where they are used, so that nothing waits for
@@ -420,6 +409,23 @@ constexpr int kOutWaves = DK / 32 < 4 ? DK / 32 : 4;
 // OUT: what becomes of the outputs.
 enum { kOutNone = 0, kOutOwn = 1, kOutSame = 2 };    // not formed; by waves of their own; by the state's waves
 
+// ------------------------------------------------------------------ scan
+//
+// One workgroup per (sequence, value head, slice of 16 NC value columns).  d_k / 32 state waves:
+// wave w keeps rows 32 w .. 32 w + 31 of the slice of H in accumulators (fp32).  A chunk goes in four
+// phases with a barrier between them: every wave's H goes to LDS as operand terms; row tile i (16
+// rows) of K H, then of W, is formed by wave i, which needs all of the one before; H' needs all of
+// U.  The outputs are formed by waves of their own, from the terms of H and U that the state waves
+// leave in LDS, in the time that those take for the next step.  Terms lie in LDS as operands are
+// read, 16 bytes to a lane (rows padded to spread over the banks took twice the reads' time);
+// accumulators have four rows to a lane, 8 bytes of that.  (Parts of K H from each wave's own rows
+// of H, added up in LDS, took 1.1 times as long: 16-byte LDS writes take 20 to 40 cycles each where
+// reads take 9.)
+//
+// A single sequence's scan is bound by what one state wave issues per chunk, one after the other,
+// so addresses are kept as running pointers, and operands of a chunk are requested while the chunk
+// before it is worked on.
+// BACK: instead of the outputs, the state before each chunk and W are kept for the gradients.
 template <int IO, int DK, int NC, int OUT>
 __global__ void __launch_bounds__(DK * 2 + (OUT == kOutOwn ? 64 * kOutWaves<DK> : 0), IO == GDN_BF16 && DK == 128 ? 2 : 1)
 rule_scan(const RuleArgs a) {
@@ -753,10 +759,6 @@ __device__ __forceinline__ void operand(f32x4 x, f32x4 y, bf16x8 (&to)[T]) {
 #pragma unroll
     for (int p = 0; p < T; ++p) to[p] = stack_pair(a[p], b[p]);
 }
-
-// Nothing is moved past this: operands that are read before it are on their way during what follows,
-// where the compiler would read each just before its use and wait for it.
-__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 template <int DK>
 __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
