@@ -1444,17 +1444,24 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a) {
                     dy[x] = mma<P, S>(o, u, dy[x]);
                     dx[x] = mma<S, S>(r, u, dx[x]);
                 }
-                // dO H^T, dR H^T and U dH'^T
+                // dO H^T, dR H^T and U dH'^T; an operand is read as soon as the one before it is used
+                bf16x8 u[R], o[P], r[S];
+                const int row = n * LD + at;
+                get8<P>(so + row, kPl, o);
+                get8<S>(sr + row, kPl, r);
+                get8<R>(su + row, kPl, u);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int row = (16 * i + n) * LD + at;
-                    bf16x8 u[R], o[P], r[S];
-                    get8<R>(su + row, kPl, u);
-                    get8<P>(so + row, kPl, o);
-                    get8<S>(sr + row, kPl, r);
+                    const int next = row + 16 * (i + 1) * LD;
+                    hold();
                     aq[i] = mma<P, S>(o, h, aq[i]);
+                    if (i < 3) get8<P>(so + next, kPl, o);
+                    hold();
                     t2[i] = mma<S, S>(r, h, t2[i]);
+                    if (i < 3) get8<S>(sr + next, kPl, r);
+                    hold();
                     t1[i] = mma<R, D>(u, d, t1[i]);
+                    if (i < 3) get8<R>(su + next, kPl, u);
                 }
             }
         }
@@ -1577,16 +1584,29 @@ __global__ void __launch_bounds__(64) rule_gates(const RuleArgs a, int parts, in
     const RuleChunk ch = rule_chunk(a, slot);
     if (ch.n == 0) return;
     const size_t val = (size_t)slot * a.Hv + hv;
-    __shared__ float z[320];
-    for (int i = lane; i < 320; i += 64) z[i] = a.zs[val * 320 + i];
-    double own = 0, to_end = 0, lead = 0;
-    float db = 0;
-    for (int w = 0; w < hsums; ++w) own += a.hs[(val * hsums + w) * kC + lane];
-    for (int s = 0; s < parts; ++s) {
-        to_end += a.pe[(val * parts + s) * kC + lane];
-        db += a.pb[(val * parts + s) * kC + lane];
-    }
+    __shared__ __attribute__((aligned(16))) float z[320];
+    float zr[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) zr[i] = a.zs[val * 320 + 64 * i + lane];
+    // the lane's column of `count` rows, eight requests at a time
+    auto column = [&](const float* rows, int count) {
+        double sum = 0;
+        for (int w = 0; w < count; w += 8) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = rows[(size_t)min(w + i, count - 1) * kC + lane];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += w + i < count ? x[i] : 0.f;
+        }
+        return sum;
+    };
+    double own = column(a.hs + val * hsums * kC, hsums);
+    double to_end = column(a.pe + val * parts * kC, parts);
+    const float db = (float)column(a.pb + val * parts * kC, parts);
+    double lead = 0;
     for (int s = lane; s < waves * 4; s += 64) lead += a.pa[val * waves * 4 + s];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) z[64 * i + lane] = zr[i];
     const double mine = to_end;
 #pragma unroll
     for (int off = 1; off < 64; off *= 2) {
@@ -1598,11 +1618,14 @@ __global__ void __launch_bounds__(64) rule_gates(const RuleArgs a, int parts, in
     double d = lead + own + to_end - mine;
     __syncthreads();
     const int T = lane / 16, n = lane % 16;
+#pragma unroll
     for (int t = 0; t < 10; ++t) {
         const int i = t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3, j = t - i * (i + 1) / 2;
         if (j == T) d += z[16 * t + n];
-        if (j < T && T <= i)
-            for (int r = T == i ? n : 0; r < 16; ++r) d += z[160 + 16 * t + r];
+        if (i == j) continue;
+        const int first = j < T && T <= i ? (T == i ? n : 0) : 16; // rows of this tile that cross row t
+#pragma unroll
+        for (int r = 0; r < 16; ++r) d += r >= first ? z[160 + 16 * t + r] : 0.f;
     }
     if (lane < ch.n) {
         const int64_t at = (ch.row0 + lane) * a.Hv + hv;
