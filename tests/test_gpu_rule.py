@@ -363,3 +363,33 @@ def test_agrees_with_the_tree_call():
     got = forward(x)
     # the tree kernels' own bound is 1e-2
     assert R.rel(got["o"], o.flatten(0, 1)) <= 1e-2 + bound("o", "bf16") and R.rel(got["S_out"], S) <= 1e-2 + F32
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_many_sequences_run_alike(io):
+    """The wider scans: the same bits with NaN patterns in the workspace, beside another call on another stream, and
+    from replays of a captured graph."""
+    x, other = many(70, 2, 4, 128, 128, io=io), make([200, 65], 2, 4, 128, 128, io, seed=5)
+    first, alone = {**forward(x), **backward(x)}, {**forward(other), **backward(other)}
+    ws = T.rule_workspace(x["dims"], x["q"].shape[0], backward=True)
+    ws.fill_(255)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        beside = {**forward(other), **backward(other)}
+    again = {**forward(x, ws=ws), **backward(x, ws=ws)}
+    torch.cuda.synchronize()
+    for name in first:
+        assert torch.equal(first[name], again[name]) and torch.equal(alone[name], beside[name]), name
+    out, f = grads_like(x), dict(o=torch.empty_like(x["v"]), S_out=torch.empty_like(x["S0"]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(x, ws=ws, **f)
+        backward(x, ws=ws, out=out)
+    for _ in range(3):
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, v in {**out, **f}.items():
+            assert torch.equal(first[name], v), name
+        forward(other)
