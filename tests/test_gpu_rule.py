@@ -130,6 +130,20 @@ def test_many_sequences(batch, hk, hv, dk, dv, io):
     check(x, {**forward(x), **backward(x)}, io)
 
 
+@pytest.mark.parametrize("skip", [0, 1])
+def test_many_sequences_in_slices_of_one_projection(skip):
+    """Rows that are whole operands as they lie, and the same ones an element further, which are not."""
+    x = many(70, 2, 4, 128, 128, io="bf16")
+    want = forward(x)
+    wide = torch.cat([x["q"][:, :0].new_zeros(x["q"].shape[0], 1, 128)] + [x[a] for a in ("q", "k", "v")], 1).flatten(1)
+    wide = torch.nn.functional.pad(wide, (0, 8)).roll(skip, 1)
+    at = lambda h, n: wide[:, (1 + h) * 128 + skip:(1 + h + n) * 128 + skip].unflatten(1, (n, 128))  # noqa: E731
+    y = {**x, "q": at(0, 2), "k": at(2, 2), "v": at(4, 4)}
+    assert all(torch.equal(x[a], y[a]) for a in ("q", "k", "v"))
+    got = forward(y)
+    assert all(torch.equal(got[a], want[a]) for a in want)
+
+
 @pytest.mark.parametrize("batch,dv", [(2, 128), (20, 128), (70, 128), (70, 33)])
 def test_outputs_in_a_wider_tensor(batch, dv):
     """Outputs at odd places between others, which stay as they were."""

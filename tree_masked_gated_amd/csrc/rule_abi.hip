@@ -91,8 +91,8 @@ size_t place(RuleArgs& a, int io, int dkp, bool back, char* at) {
     take(a.kt, keys * tile);
     take(a.tm, vals * kSum * tri);
     take(a.coef, vals * 3 * kC * sizeof(float));
-    take(a.qf, keys * tile);
     if (!back) {
+        take(a.qf, keys * tile);
         take(a.ym, vals * round * tri);
         return used;
     }

@@ -46,6 +46,7 @@ struct RuleArgs {
     Rows q, k, v, o, d_o, dq, dk_out, dv_out; // strides in elements
     int vq, vk, vdo;                         // rows of q, k, d_o can be read 16 bytes at a time
     int vo;                                  // rows of o can be written 8 bytes at a time
+    int direct;                              // the scan reads q and k from their rows
     const float* beta;
     const float* g;
     const float* S0;

@@ -18,7 +18,7 @@ constexpr int kTp = kC + 8;
 // substitution, the others by fp32 matrix instructions) and kept as bf16 terms.
 //
 // Bound by what it writes: 8192 rows of 16 / 32 heads of 128, bf16, 81 us for 230 MB written and 62
-// MB read; 25331 rows in 24 sequences, 236 us for 730 and 187 MB (3.9 TB/s).
+// MB read; 25331 rows in 24 sequences, without K's and Q's operands, 201 us for 520 and 187 MB.
 template <int IO, int DK, bool BACK>
 __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, R = kRound<IO>, KS = DK / 32, NT = DK / 16, LD = DK + 8;
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
         kfr[s] = load_row8<IO>(a.k.p, grow * a.k.row + (int64_t)hk * a.k.head, 32 * s + 8 * q4, a.dk, a.vk, live);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
-            store_frag(a.kf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, kfr[s].p[p]);
+            if (!a.direct) store_frag(a.kf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, kfr[s].p[p]);
             *reinterpret_cast<bf16x8*>(&rows[p][row][32 * s + 8 * q4]) = kfr[s].p[p];
         }
     }
@@ -55,9 +55,10 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
         qfr[s] = load_row8<IO>(a.q.p, grow * a.q.row + (int64_t)hk * a.q.head, 32 * s + 8 * q4, a.dk, a.vq, live);
+        if (!BACK && !a.direct)
 #pragma unroll
-        for (int p = 0; p < P; ++p)
-            store_frag(a.qf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, qfr[s].p[p]);
+            for (int p = 0; p < P; ++p)
+                store_frag(a.qf + key * kTile + ((p * 4 + wv) * KS + s) * kFrag, lane, qfr[s].p[p]);
     }
     __syncthreads();
     // the lower row tiles of K K^T and Q K^T
@@ -730,7 +731,7 @@ rule_scan(const RuleArgs a) {
 // waited for where two parts of work have passed since.  bf16 rows only: three terms of every
 // operand would not fit.  Outputs are formed transposed, so that a lane has four columns of a row.
 //
-// 81 KB of LDS: two workgroups to a compute unit.  24 prompts, 25331 rows, 32 heads: 480 us, 16 K
+// 81 KB of LDS: two workgroups to a compute unit.  24 prompts, 25331 rows, 32 heads: 490 us, 16 K
 // cycles a chunk for the two waves of a SIMD, whose matrix instructions are 5.8 K; between them stand
 // the terms of H and the waits at the chunk's three barriers.  (rule_scan with two column blocks and
 // the outputs by the state's waves: 555 us; every operand read just before its use: 570 us.)
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
             const int i = 16 * t + 4 * q4 + r;
             h[t][r] = a.S0 && i < a.dk && col < a.dv ? a.S0[state + i] : 0.f;
         }
-    const char *pk = a.kf + key, *pq = a.qf + key, *pt = a.kt + key, *pm = a.tm + val * nM * kFrag, *py = a.ym + val * nY * kFrag;
+    const char *pt = a.kt + key, *pm = a.tm + val * nM * kFrag, *py = a.ym + val * nY * kFrag;
     const float* pc = a.coef + val * 3 * kC;
     uint16_t v[4][4];                                // of the next chunk: rows 16 i + 4 q4 + r
     const uint16_t* pv = reinterpret_cast<const uint16_t*>(a.v.p) + (seq.row0 + 4 * q4) * a.v.row + hv * a.v.head + min(col, a.dv - 1);
@@ -805,9 +806,30 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
     auto send_coef = [&](int c) {
         if (wv == 0 && lane < 3 * kC / 4) send16((const char*)pc, lds_at(sc) + (c & 1) * sizeof(sc[0]), lane * 16);
     };
-    auto send_k = [&] {
-        send<nK>(pk, lds_at(sk), wv, lane);
-        send<nK>(pq, lds_at(sq), wv, lane);
+    // K and Q, as prepared or from the rows themselves: a lane's 16 bytes are eight elements of a row either
+    // way.  Rows past the sequence's end are its last row; their coefficients are 0, their outputs not stored.
+    const int direct = a.direct;
+    auto key_rows = [&](const Rows& x, const char* prepared) {
+        return direct ? x.p + (seq.row0 * x.row + hk * x.head) * 2 : prepared + key;
+    };
+    const char *pk = key_rows(a.k, a.kf), *pq = key_rows(a.q, a.qf);
+    auto send_rows = [&](const Rows& x, const char* from, uint32_t to, int rows) {
+        const uint32_t row = (uint32_t)x.row * 2;
+        const bool part = direct && rows < kC;
+#pragma unroll
+        for (int y = 0; y < nK / 4; ++y) {
+            const int f = wv + 4 * y, i = f / KS, s = f % KS;
+            if (part)
+                send16(from + 64 * s, to + f * kFrag, min(16 * i + n, rows - 1) * row + 16 * q4);
+            else if (direct)
+                send16(from + 16 * i * (size_t)row + 64 * s, to + f * kFrag, n * row + 16 * q4);
+            else
+                send16(from + f * kFrag, to + f * kFrag, lane * 16);
+        }
+    };
+    auto send_k = [&](int rows) {
+        send_rows(a.k, pk, lds_at(sk), rows);
+        send_rows(a.q, pq, lds_at(sq), rows);
     };
     auto send_t = [&] {
         send<nT>(pt, lds_at(st), wv, lane);
@@ -827,7 +849,7 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
         }
     };
     if (chunks > 0) {
-        send_k();
+        send_k(chunks > 1 ? kC : tail);
         send_coef(0);
         load_v(chunks > 1 ? kC : tail);
         send<nM>(pm, lds_at(sm), wv, lane);
@@ -881,10 +903,10 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
         }
         wait_vmem_all();                             // K^T and Y
         lds_barrier();                               // K and Q are free
-        pk += more ? key_step : 0;
-        pq += more ? key_step : 0;
+        pk += !more ? 0 : direct ? kC * 2 * a.k.row : key_step;
+        pq += !more ? 0 : direct ? kC * 2 * a.q.row : key_step;
         pc += more ? co_step : 0;
-        send_k();
+        send_k(c + 2 < chunks ? kC : tail);
         send_coef(c + 1);
         pv += more ? kC * a.v.row : 0;
         load_v(c + 2 < chunks ? kC : tail);
@@ -1669,8 +1691,15 @@ hipError_t scan_launch(const RuleArgs& a, hipStream_t stream) {
 template <int DK>
 constexpr int64_t kFewSlices = kPlaces * 128 / DK;
 template <int IO, int DK>
-hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
+hipError_t rule_forward_launch(const RuleArgs& args, hipStream_t stream) {
+    RuleArgs a = args;
     hipError_t e = hipSuccess;
+    const bool wide = IO == GDN_BF16 && DK <= 128 && slices_of_16(a) > 4 * kPlaces;
+    // The wide scan takes keys and queries from their rows where these are whole operands, 16 bytes at a time,
+    // and 64 of them within a lane's 32-bit offset (25331 rows, 16 heads of 128: 608 us for
+    // both kernels, 623 through prepared operands, which are 210 MB more to write).
+    constexpr int64_t kNear = 1 << 24;
+    a.direct = wide && a.dk == DK && a.vk && a.vq && a.k.row <= kNear && a.q.row <= kNear;
     if (a.T > 0)
         e = launch(rule_prepare<IO, DK, false>, dim3(a.n_slots, a.Hk), dim3(256), 0, stream, a);
     if (e != hipSuccess) return e;
@@ -1679,7 +1708,7 @@ hipError_t rule_forward_launch(const RuleArgs& a, hipStream_t stream) {
     } else {
         if (slices_of_16(a) <= kFewSlices<DK>) return scan_launch<IO, DK, 1, kOutOwn>(a, stream);
         if constexpr (IO == GDN_BF16)
-            if (slices_of_16(a) > 4 * kPlaces) return scan_wide_launch<DK>(a, stream);
+            if (wide) return scan_wide_launch<DK>(a, stream);
         return scan_launch<IO, DK, 2, kOutSame>(a, stream);
     }
 }
