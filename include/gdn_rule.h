@@ -20,7 +20,7 @@
  *    can be slices of one projection's output.  They need their elements' alignment alone
  *    (rows and heads at multiples of 16 bytes are read fastest); output rows must not
  *    overlap each other.
- *  - beta and g are [rows][h_v] fp32, contiguous; g in (0, 1].
+ *  - beta and g are [rows][h_v] fp32, contiguous; g in [0, 1].
  *  - Sequences are packed: sequence b owns rows offsets[b] .. offsets[b+1] - 1 (device
  *    int32 [B + 1], non-decreasing from 0, 4-byte aligned), 0 rows allowed, n_rows rows in
  *    all tensors.  A sequence whose offsets are unusable (offsets[b] < 0, fewer than 0

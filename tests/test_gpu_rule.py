@@ -189,6 +189,18 @@ def test_gates(gates):
     check(x, {**forward(x), **backward(x)}, "f32")
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gates_of_zero(io):
+    """A gate of 0 forgets everything before its row, and its gradient with regard to ln g is 0."""
+    x = make([70, 130, 1], 2, 4, 64, 64, io)
+    zero = torch.rand(x["g"].shape, device="cuda", generator=torch.Generator("cuda").manual_seed(8)) < 0.1
+    zero[[0, 64, 70, 199], :2] = True
+    x["g"][zero] = 0
+    got = {**forward(x), **backward(x)}
+    check(x, got, io)
+    assert (got["dlog_g"][zero] == 0).all()
+
+
 def test_write_strengths():
     """No writes at all, whole writes, and the same key every time."""
     x = make([100, 80], 1, 2, 64, 64, "f32", gates="none")

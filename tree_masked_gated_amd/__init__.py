@@ -751,7 +751,7 @@ def rule_workspace(d: RuleDims, n_rows, backward=False, device="cuda"):
     return torch.empty(max(gdn_rule_workspace_bytes(d, n_rows, backward), 16), dtype=torch.uint8, device=device)
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _rule_bytes_of(sizes, T, backward):
     return gdn_rule_workspace_bytes(RuleDims(*sizes), T, backward)
 
@@ -868,7 +868,7 @@ def _logits(x, d, name):
     return x.data_ptr()
 
 
-@functools.lru_cache(maxsize=None)
+@functools.lru_cache(maxsize=4096)
 def _score_bytes_of(*sizes):
     return gdn_score_workspace_bytes(ScoreDims(*sizes))
 

@@ -142,7 +142,9 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
             const bool in = lane < ch.n;
             const int64_t at = (ch.row0 + (in ? lane : 0)) * a.Hv + hv;
             const float b = in ? a.beta[at] : 0.f;
-            double x = in ? (double)log2f(a.g[at]) : 0.0;
+            // A gate of 0: differences across it have no power of 2 in fp32, others keep theirs.
+            const float g = a.g[at];
+            double x = !in ? 0.0 : g == 0.f ? -1000.0 : (double)log2f(g);
 #pragma unroll
             for (int off = 1; off < 64; off *= 2) {
                 const double y = __shfl_up(x, off);
