@@ -33,10 +33,9 @@
 #include "attn_common.hpp"
 #include "gdn_rule.h"
 #include "mfma_tiles.hpp"
+#include "rule_schedule.hpp"
 
 namespace gdn {
-
-constexpr int kC = 64;
 
 struct RuleArgs {
     int B, Hk, Hv, group, dk, dv, n_slots;   // n_slots: chunk slots, T / kC + B

@@ -298,10 +298,10 @@ struct Rows4 {
 #pragma unroll
         for (int r = 0; r < 4; ++r) off[r] = (row + r) * from.row;
     }
-    // the places of a chunk of `rows` rows, fewer than kC
-    __device__ __forceinline__ void last(int64_t stride, int rows) {
+    // the places of a chunk of `rows` rows
+    __device__ __forceinline__ void places(int64_t stride, int rows) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) off[r] = min(row + r, rows - 1) * stride;
+        for (int r = 0; r < 4; ++r) off[r] = row_in(row + r, rows) * stride;
     }
     __device__ __forceinline__ void load(int64_t chunk) {
         const E* p = at + chunk * step;
@@ -453,8 +453,8 @@ rule_scan(const RuleArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q4 = lane >> 4;
     const RuleSeq seq = rule_seq(a, b);
-    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
-    const int tail = seq.n - (chunks - 1) * kC;      // rows of the last chunk
+    const int chunks = chunks_of(seq.n), base = slot_base(seq.row0, b);
+    const int tail = last_rows(seq.n);          // rows of the last chunk
     const int col0 = sl * 16 * NC + n;               // this lane's columns: col0 + 16 c
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
@@ -545,15 +545,13 @@ rule_scan(const RuleArgs a) {
         if constexpr (kHold)
 #pragma unroll
             for (int s = 0; s < KS; ++s) load_k(pk, s, s);
-        const bool part = c == chunks - 1 && tail < kC;
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii) {
             ca[ii] = *reinterpret_cast<const f32x4*>(pca + 16 * deal.tile(ii) + 4 * q4);
 #pragma unroll
-            for (int x = 0; x < NX; ++x) {
-                if (part) v[ii][x].last(a.v.row, tail);
-                v[ii][x].load(c);
-            }
+            for (int x = 0; x < NX; ++x)
+                request_forward(
+                    seq.n, c, [&](int rows) { v[ii][x].places(a.v.row, rows); }, [&](int at) { v[ii][x].load(at); });
         }
     };
     auto load_c = [&] {
@@ -643,7 +641,7 @@ rule_scan(const RuleArgs a) {
             }
         pk += more ? key_step : 0;
         pca += more ? co_step : 0;
-        load_b(more ? c + 1 : c);
+        load_b(after(seq.n, c));
         if constexpr (OUT == kOutSame) {
             out.pq += more ? key_step : 0;
             out.load_q(lane);
@@ -782,8 +780,8 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q4 = lane >> 4;
     const RuleSeq seq = rule_seq(a, b);
-    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
-    const int tail = seq.n - (chunks - 1) * kC;
+    const int chunks = chunks_of(seq.n), base = slot_base(seq.row0, b);
+    const int tail = last_rows(seq.n);
     const int block = sl * kWide + 16 * wv, col = block + n; // the wave's columns; this lane's
     const bool work = block < a.dvp;                 // columns past d_v have zeros to work on, past dvp no place
     const size_t key = ((size_t)base * a.Hk + hk) * nK * kFrag, val = (size_t)base * a.Hv + hv;
@@ -1070,7 +1068,7 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
     const int n = lane & 15, q4 = lane >> 4;
     const D deal{wv};
     const RuleSeq seq = rule_seq(a, b);
-    const int chunks = (seq.n + kC - 1) / kC, base = slot_base(seq.row0, b);
+    const int chunks = chunks_of(seq.n), base = slot_base(seq.row0, b);
     const int col0 = sl * 16 * NC + n;
     constexpr size_t kTile = (size_t)P * 4 * KS * kFrag;
     constexpr size_t kTri = (size_t)kTriFrags * kFrag;
@@ -1163,12 +1161,11 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
                     qt[t][s][p] = load_frag(a.qt + key + ((p * NT + 2 * wv + t) * 2 + s) * kFrag, lane);
                 }
     };
-    const int tail = seq.n - (chunks - 1) * kC;
     auto places = [&](int rows) {
 #pragma unroll
         for (int ii = 0; ii < NI; ++ii)
 #pragma unroll
-            for (int x = 0; x < NX; ++x) raw[ii][x].last(a.d_o.row, rows);
+            for (int x = 0; x < NX; ++x) raw[ii][x].places(a.d_o.row, rows);
     };
 #pragma unroll
     for (int ii = 0; ii < NI; ++ii)
@@ -1177,16 +1174,14 @@ __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) r
             raw[ii][x].begin(a.d_o, seq.row0, hv * a.d_o.head, 16 * deal.tile(ii) + 4 * q4, col0 + 16 * deal.block(x), a.dv);
     wait_vmem_all();
     if (chunks > 0) {
-        places(tail);
-        load_a(chunks - 1);
-        places(kC);
+        request_back_first(seq.n, places, load_a);
         load_b(chunks - 1);
         load_c(chunks - 1);
         load_d(chunks - 1);
     }
     for (int c = chunks - 1; c >= 0; --c) {
         const size_t val = val_of(c);
-        const int next = max(c - 1, 0);
+        const int next = before(c);
         // dH' and dO to LDS, and a_C <H, dH'>
         f32x4 d_o[NI][NX];
 #pragma unroll
