@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
     __shared__ __attribute__((aligned(16))) float xs[kC][TP];
     __shared__ __attribute__((aligned(16))) float ts[kC][TP];
     __shared__ double gam[kC];
-    __shared__ float bet[kC];
+    __shared__ __attribute__((aligned(16))) float bet[kC];
 
     const int slot = blockIdx.x, hk = blockIdx.y;
     const RuleChunk ch = rule_chunk(a, slot);
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(256, 2) rule_scan_wide(const RuleArgs a) {
     constexpr int nK = 4 * KS, nM = kTriFrags * S, nT = 2 * NT, nY = kTriFrags * R;
     __shared__ __attribute__((aligned(16))) char sk[nK * kFrag], sq[nK * kFrag], sm[nM * kFrag], st[nT * kFrag],
         sy[nY * kFrag];
-    __shared__ float sc[2][3 * kC];
+    __shared__ __attribute__((aligned(16))) float sc[2][3 * kC];
 
     int b, hv, sl;
     scan_place<IO, DK>(a, (a.dvp + kWide - 1) / kWide, b, hv, sl);
@@ -1355,7 +1355,7 @@ __global__ void __launch_bounds__(DK * 4) rule_join(const RuleArgs a) {
     __shared__ __attribute__((aligned(16))) uint16_t lds[NB * kBlk];
     static_assert(kBlk >= (S + 2 * D) * kSq, "the matrices fit");
     __shared__ double gam[kC];
-    __shared__ float coef[3][kC];
+    __shared__ __attribute__((aligned(16))) float coef[3][kC];
     uint16_t *sp = lds, *spt = lds + S * kSq, *sg = spt + D * kSq;
 
     const int slot = blockIdx.x, hk = blockIdx.y;
