@@ -52,7 +52,7 @@ int gdn_token_scores(const gdn_score_dims* dims, const void* logits, const int32
                      hipStream_t stream);
 
 /*
- * Gradient of the logits, from lse and entropy as gdn_token_scores wrote them:
+ * Gradient of the logits, from lse and entropy as gdn_token_scores wrote them for these logits:
  *
  *     d_x_j = -p_j (d_logp + sum_c d_top_logp_c + d_entropy (ln p_j + entropy))
  *             + [j = token] d_logp + sum_c [j = top_tok_c] d_top_logp_c
@@ -63,7 +63,9 @@ int gdn_token_scores(const gdn_score_dims* dims, const void* logits, const int32
  *   d_top_logp [rows][topk] fp32  part in the gradient.  Both NULL: no such term
  *   d_logits   [rows][vocab] io  out, row_stride elements apart; may be logits
  *
- * A token outside [0, vocab) has no part in the gradient.
+ * A token outside [0, vocab) has no part in the gradient.  ln p_j is x_j - lse, with what lse's rounding
+ * leaves of it (2^-24 |lse|); where |lse| >= 4096, as in rows that hold a mask's value alone, it
+ * comes of the row's logits again.
  */
 int gdn_token_scores_backward(const gdn_score_dims* dims, const void* logits, const int32_t* tokens, const float* lse,
                               const float* entropy, const float* d_logp, const float* d_entropy,

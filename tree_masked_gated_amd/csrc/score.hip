@@ -390,10 +390,40 @@ struct ScoreBackArgs {
     char* d_logits;
 };
 
+// From here on lse's own rounding, half a step of it, is 2^-13 of every p and more, and nothing of ln s
+// is left in it where a row holds no more than a mask's value.
+constexpr float kFarLse = 4096.f;
+
+// m and s of all of a row, by one workgroup of NT threads, in every thread.
+template <int IO, int NT>
+__device__ Stat whole_row(const Span<IO>& sp) {
+    __shared__ Stat stats[NT / 64];
+    Stat st{-FLT_MAX, 0.f, 0.f};
+    sp.each(NT, __builtin_nanf(""), [&](float x, int) {
+        if (x > st.m) st.raise(x);
+        st.add(x);
+    });
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+        Stat o;
+        o.m = __shfl_xor(st.m, off);
+        o.s = __shfl_xor(st.s, off);
+        o.t = __shfl_xor(st.t, off);
+        st.join(o);
+    }
+    if (threadIdx.x % 64 == 0) stats[threadIdx.x / 64] = st;
+    __syncthreads();
+    st = stats[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) st.join(stats[w]);
+    return st;
+}
+
 // d x_j = -p_j (sum of the given gradients + d_entropy (ln p_j + entropy)), plus the given
 // gradients at their own tokens: these few elements are formed again, whole, by the threads of
 // their numbers once the part is written.  Their logits are read before it is, since the
-// gradient may take the logits' place.
+// gradient may take the logits' place.  ln p_j is x_j - lse; of a row with a far lse (kFarLse) the first
+// part's workgroup takes all, and has ln p_j = (x_j - m) - ln s from the logits.
 template <int IO>
 __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
     constexpr int NT = 256, U = 4, e = IO == GDN_BF16 ? 2 : 4;
@@ -402,8 +432,9 @@ __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
     const int64_t row = blockIdx.x / a.parts;
     const int part = blockIdx.x % a.parts, tid = threadIdx.x;
     const size_t at = (size_t)(row * a.stride) * e;
-    const Span<IO> sp(a.logits + at, part * a.part, min(a.vocab, (part + 1) * a.part));
+    Span<IO> sp(a.logits + at, part * a.part, min(a.vocab, (part + 1) * a.part));
     char* out = a.d_logits + at;
+    const float lse = a.lse[row];
     const int points = 1 + (a.top_tok ? a.topk : 0);
     int mine = -1;
     float own = 0.f;
@@ -426,9 +457,18 @@ __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
     __syncthreads();
     float all = 0.f;
     for (int i = 0; i < points; ++i) all += add[i];
-    const float ge = a.d_entropy ? a.d_entropy[row] : 0.f, h = a.d_entropy ? a.entropy[row] : 0.f, lse = a.lse[row];
+    const float ge = a.d_entropy ? a.d_entropy[row] : 0.f, h = a.d_entropy ? a.entropy[row] : 0.f;
+    float from = lse, log_s = 0.f;                   // ln p = (x - from) - log_s
+    if (fabsf(lse) >= kFarLse) {
+        if (part > 0) return;
+        sp = Span<IO>(a.logits + at, 0, a.vocab);
+        mine = tid < points ? tok[tid] : -1;
+        if (mine >= 0) own = ld_io<IO>(sp.row, mine);
+        const Row r(whole_row<IO, NT>(sp));
+        from = r.m, log_s = r.log_s;
+    }
     auto grad = [&](float x) {
-        const float l = x - lse, p = __builtin_amdgcn_exp2f(l * kLog2E);
+        const float l = (x - from) - log_s, p = __builtin_amdgcn_exp2f(l * kLog2E);
         return -p * (all + ge * (fmaxf(l, kFar) + h));
     };
     if (tid < sp.head) st_io<IO>(out, sp.lo + tid, grad(ld_io<IO>(sp.row, sp.lo + tid)));
