@@ -390,6 +390,8 @@ struct ScoreBackArgs {
     char* d_logits;
 };
 
+// e^kNever is 0 in fp32: what stands in for ln p below it, near enough that no gradient carries it to infinity.
+constexpr float kNever = -200.f;
 // From here on lse's own rounding, half a step of it, is 2^-13 of every p and more, and nothing of ln s
 // is left in it where a row holds no more than a mask's value.
 constexpr float kFarLse = 4096.f;
@@ -469,7 +471,7 @@ __global__ void __launch_bounds__(256) score_back(const ScoreBackArgs a) {
     }
     auto grad = [&](float x) {
         const float l = (x - from) - log_s, p = __builtin_amdgcn_exp2f(l * kLog2E);
-        return -p * (all + ge * (fmaxf(l, kFar) + h));
+        return -p * (all + ge * (fmaxf(l, kNever) + h));
     };
     if (tid < sp.head) st_io<IO>(out, sp.lo + tid, grad(ld_io<IO>(sp.row, sp.lo + tid)));
     if (tid < sp.hi - sp.tail()) st_io<IO>(out, sp.tail() + tid, grad(ld_io<IO>(sp.row, sp.tail() + tid)));
