@@ -158,11 +158,16 @@ def _ptr(x, shape, dtype, name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, x=None):
+    """The handle of the stream, or of the current one, on whose device a tensor x has to be then."""
     if stream is None:
+        device = torch.cuda.current_device()
+        if x is not None and x.get_device() != device:
+            raise ValueError(f"tensors on device {x.get_device()}, and device {device} is the current device: its "
+                             "stream cannot serve them")
         if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -784,7 +789,7 @@ def gdn_rule_forward(d: RuleDims, offsets, q, k, v, beta, g, o, workspace, S0=No
         d, _ints(offsets, (B + 1,), "offsets"), T, _f32s(S0, state, "S0"), _attn_rows(q, T, hk, dk, io, "q"),
         _attn_rows(k, T, hk, dk, io, "k"), _attn_rows(v, T, hv, dv, io, "v"), _f32s(beta, (T, hv), "beta"),
         _f32s(g, (T, hv), "g"), _attn_rows(o, T, hv, dv, io, "o"), _f32s(S_out, state, "S_out"),
-        _rule_workspace(workspace, d, T, False), _stream(stream))
+        _rule_workspace(workspace, d, T, False), _stream(stream, q))
     if rc:
         raise GdnError(rc, "gdn_rule_forward")
 
@@ -802,7 +807,7 @@ def gdn_rule_backward(d: RuleDims, offsets, q, k, v, beta, g, d_o, dq, dk, dv, d
         d, _ints(offsets, (B + 1,), "offsets"), T, _f32s(S0, state, "S0"), keys(q, "q"), keys(k, "k"), vals(v, "v"),
         _f32s(beta, gate, "beta"), _f32s(g, gate, "g"), vals(d_o, "d_o"), _f32s(dS_out, state, "dS_out"),
         keys(dq, "dq"), keys(dk, "dk"), vals(dv, "dv"), _f32s(dbeta, gate, "dbeta"), _f32s(dlog_g, gate, "dlog_g"),
-        _f32s(dS0, state, "dS0"), _rule_workspace(workspace, d, T, True), _stream(stream))
+        _f32s(dS0, state, "dS0"), _rule_workspace(workspace, d, T, True), _stream(stream, q))
     if rc:
         raise GdnError(rc, "gdn_rule_backward")
 
@@ -816,7 +821,7 @@ def gdn_rule_step(d: RuleDims, q, k, v, beta, g, state, o, slot=None, stream=Non
         d, None if slot is None else _ints(slot, (B,), "slot"), n, _attn_rows(q, B, hk, dk, io, "q"),
         _attn_rows(k, B, hk, dk, io, "k"), _attn_rows(v, B, hv, dv, io, "v"), _f32s(beta, (B, hv), "beta"),
         _f32s(g, (B, hv), "g"), _f32s(state, (n, hv, dv, dk), "state"), _attn_rows(o, B, hv, dv, io, "o"),
-        _stream(stream))
+        _stream(stream, q))
     if rc:
         raise GdnError(rc, "gdn_rule_step")
 
@@ -890,7 +895,7 @@ def gdn_token_scores(d: ScoreDims, logits, tokens, logp, entropy, lse, workspace
     rc = _lib.gdn_token_scores(
         d, _logits(logits, d, "logits"), _tokens(tokens, n, "tokens"), _f32s(logp, n, "logp"),
         _f32s(entropy, n, "entropy"), _f32s(lse, n, "lse"), _f32s(top_logp, k, "top_logp"),
-        _tokens(top_tok, k, "top_tok"), workspace.data_ptr(), _stream(stream))
+        _tokens(top_tok, k, "top_tok"), workspace.data_ptr(), _stream(stream, logits))
     if rc:
         raise GdnError(rc, "gdn_token_scores")
 
@@ -905,6 +910,6 @@ def gdn_token_scores_backward(d: ScoreDims, logits, tokens, lse, entropy, d_logp
         d, _logits(logits, d, "logits"), _tokens(tokens, n, "tokens"), _f32s(lse, n, "lse"),
         _f32s(entropy, n, "entropy"), _f32s(d_logp, n, "d_logp"), _f32s(d_entropy, n, "d_entropy"),
         _tokens(top_tok, k, "top_tok"), _f32s(d_top_logp, k, "d_top_logp"), _logits(d_logits, d, "d_logits"),
-        _stream(stream))
+        _stream(stream, logits))
     if rc:
         raise GdnError(rc, "gdn_token_scores_backward")
