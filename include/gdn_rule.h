@@ -25,13 +25,21 @@
  *    int32 [B + 1], non-decreasing from 0, 4-byte aligned), 0 rows allowed, n_rows rows in
  *    all tensors.  A sequence whose offsets are unusable (offsets[b] < 0, fewer than 0
  *    rows, rows past n_rows) has none of its rows read or written, and its state is
- *    passed through.  Rows that belong to no sequence are neither read nor written.
+ *    passed through.  The others keep their results if each usable one begins at or after the
+ *    end of the usable ones before it; where one begins earlier, as the third of offsets 0, 1000,
+ *    50, 200 does, it and those that it goes back over have undefined results (still, nothing
+ *    but their rows and states is written).  Rows that belong to no sequence are neither read
+ *    nor written.
+ *  - Elements have to be finite.  NaN or an infinity in a row can reach all results of its sequence,
+ *    those of up to 63 rows before it in the forward pass included; other sequences keep theirs.
  *  - Outputs must not overlap inputs, except that S_out may be S0 and dS0 may be dS_out.
  *
  * Sizes: 1 <= d_k, d_v <= 256; h_k >= 1; h_v a multiple of h_k, <= 32768; batch <= 2^20;
  * n_rows / 64 + batch < 2^21; batch h_v d_v / 16 < 2^22 (d_v rounded up to 32).
  * gdn_rule_step: batch <= 65535.  batch = 0 launches nothing; row tensors of n_rows = 0 may
- * be NULL.
+ * be NULL.  Every chunk of 64 rows looks for its sequence among all offsets, 64 at a time, and every
+ * sequence of a step with slots among those before it: beyond some thousand sequences a call
+ * takes time with the square of their number.
  *
  * Rounding.  States, sums, gates and their gradients are fp32.  The products run on
  * bf16 matrix instructions with fp32 sums; fp32 factors enter them as sums of bf16
