@@ -15,7 +15,9 @@
  * without a finite logit, with +inf or with NaN has NaN or infinite results, as the
  * formulas give them; no other row is touched by it.
  *
- * Conventions are those of gdn_tree.h.  Sums and results are fp32.
+ * Conventions are those of gdn_tree.h: every pointer is 16-byte aligned (GDN_ERR_ALIGN), so that
+ * labels from a tensor's second element on have to be copied; the rows of logits may lie at any
+ * distance.  Sums and results are fp32.
  */
 #ifndef GDN_SCORE_H
 #define GDN_SCORE_H
@@ -26,8 +28,9 @@
 extern "C" {
 #endif
 
-/* rows >= 0 (0 launches nothing), 1 <= vocab <= 2^24, 0 <= topk <= min(64, vocab),
- * row_stride >= vocab: elements between rows of logits and of their gradient. */
+/* 0 <= rows <= 2^22 (0 launches nothing), 1 <= vocab <= 2^24, rows ceil(vocab / 16384) < 2^24,
+ * 0 <= topk <= min(64, vocab), vocab <= row_stride <= 2^40: elements between rows of logits and of their
+ * gradient.  Others: GDN_ERR_DIMS. */
 typedef struct {
     int64_t rows, row_stride;
     int32_t vocab, topk, io_dtype;
