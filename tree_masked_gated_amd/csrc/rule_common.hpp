@@ -16,18 +16,15 @@
 //     dQ = a dO H^T + P K,  P = lower(D o dO U^T)
 //     dK = P^T Q + (G + G^T) K + e^(Gamma_C - Gamma) U dH'^T - a beta dR H^T,
 //                                                 G = strict_lower(-beta_i D_ij dR_i . U_j)
-//     d ln g_t: rule_join and rule_gates say how
+//     d ln g_t: over the paths that cross row t, as rule_join's comment says
 //
 // Both inverses come of one matrix, M = L (I + beta L)^-1: W = F - M (beta F) and
 // dR = dU - M^T (beta dU).  The unit parts stay in fp32, and a beta of 0 needs no division.
 //
-// (the last line: d ln g_t is <P_t, dP_t>, and <S_t, dS_t> changes over a token by what the
-// token writes, v . dv, and what it reads, o . do).
-//
-// Five kernels: rule_prepare forms M and Y of all chunks at once; rule_scan walks each
+// rule_prepare forms M and Y of all chunks at once; rule_scan, or rule_scan_wide for many slices, walks each
 // sequence's chunks forward, a workgroup for a slice of the value columns; rule_scan_back
-// walks them backward; rule_join forms dQ and dK
-// of all chunks at once, and rule_gates the gates' gradients.
+// walks them backward; rule_join forms dQ and dK of all chunks at once, and rule_gates
+// the gates' gradients.
 #pragma once
 
 #include "attn_common.hpp"

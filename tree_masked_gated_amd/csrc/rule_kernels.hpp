@@ -17,8 +17,8 @@ constexpr int kTp = kC + 8;
 // its value heads makes its M and Y of them.  M is formed in fp32 (diagonal blocks by
 // substitution, the others by fp32 matrix instructions) and kept as bf16 terms.
 //
-// Bound by what it writes: 8192 rows of 16 / 32 heads of 128, bf16, 81 us for 230 MB written and 62
-// MB read; 25331 rows in 24 sequences, without K's and Q's operands, 201 us for 520 and 187 MB.
+// Bound by what it writes: 8192 rows of 16 / 32 heads of 128, bf16, 84 us for 230 MB written and 62
+// MB read; 25331 rows in 24 sequences, without K's and Q's operands, 181 us for 518 and 183 MB.
 template <int IO, int DK, bool BACK>
 __global__ void __launch_bounds__(256) rule_prepare(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, R = kRound<IO>, KS = DK / 32, NT = DK / 16, LD = DK + 8;
@@ -244,7 +244,7 @@ __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 // The place-th longest sequence, where there are more workgroups than places for them: those that
 // take longest begin first, so that none begins when the rest are nearly done.  A wave orders up to
 // 64 sequences by itself; with more, what a place gets averages out.  (24 prompts of 0 to 2048 rows,
-// 32 heads: 553 us in the order of the batch, 480 longest first.)
+// 32 heads, wide scan: 505 us in the order of the batch, 443 longest first.)
 constexpr int kPlaces = 512;                         // two workgroups to a compute unit
 __device__ __forceinline__ int longest(const RuleArgs& a, int place) {
     if (gridDim.x <= kPlaces || a.B > 64) return place;
@@ -731,10 +731,10 @@ rule_scan(const RuleArgs a) {
 // waited for where two parts of work have passed since.  bf16 rows only: three terms of every
 // operand would not fit.  Outputs are formed transposed, so that a lane has four columns of a row.
 //
-// 81 KB of LDS: two workgroups to a compute unit.  24 prompts, 25331 rows, 32 heads: 490 us, 16 K
-// cycles a chunk for the two waves of a SIMD, whose matrix instructions are 5.8 K; between them stand
-// the terms of H and the waits at the chunk's three barriers.  (rule_scan with two column blocks and
-// the outputs by the state's waves: 555 us; every operand read just before its use: 570 us.)
+// 81 KB of LDS: two workgroups to a compute unit.  24 prompts, 25331 rows, 32 heads: 443 us, in which
+// matrix instructions take a third of the cycles; between them stand the terms of H and the waits
+// at the chunk's three barriers.  (rule_scan with two column blocks and the outputs by the state's
+// waves: 500 us.  K and Q through prepared operands: 418 us, and rule_prepare 226 in place of 181.)
 constexpr int kWide = 64;
 
 // 16 bytes a lane from memory to LDS.  from and to are the wave's; at: the lane's place from there.
@@ -1047,8 +1047,8 @@ __device__ __forceinline__ float row_scan(float x) {
 // rule_scan's shape from the last chunk to the first, the accumulators holding the slice of dH.
 // It leaves dH' and dR of every chunk for rule_join, writes dV, and leaves the slice's parts of
 // dbeta and of the terms of d ln g that reach the chunk's end: e^(Gamma_C - Gamma_j) k_j . dH' u_j
-// of every row, and a_C <H, dH'>.  4 sequences, 6727 rows, 32 heads of 128, bf16: 303 us for 600 MB
-// read and 390 written (3.3 TB/s); the longest sequence's 32 chunks are 9.5 us each.
+// of every row, and a_C <H, dH'>.  4 sequences, 6727 rows, 32 heads of 128, bf16: 301 us for 600 MB
+// read and 390 written (3.3 TB/s); the longest sequence's 32 chunks are 9.4 us each.
 template <int IO, int DK, int NC>
 __global__ void __launch_bounds__(DK * 2, IO == GDN_BF16 && DK >= 128 ? 2 : 1) rule_scan_back(const RuleArgs a) {
     constexpr int P = kPlanes<IO>, KS = DK / 32, NW = KS, NT = DK / 16;
@@ -1678,13 +1678,20 @@ hipError_t scan_launch(const RuleArgs& a, hipStream_t stream) {
     return launch(rule_scan<IO, DK, NC, OUT>, dim3(a.B * a.Hv * (a.dvp / (16 * NC))), dim3(waves * 64), 0, stream, a);
 }
 
-// Which scan, by the number of slices of 16 columns (d_k 128, bf16; us for uneven lengths up to 2048):
-//   slices                    512    768   1024   2048   4096
-//   outputs by own waves       86     81    138    242    308   narrowest, shortest chunk of all
-//   two column blocks          91     91    120    170    187   half the operands read per column
-//   wide                      148    144    146    196    168   a quarter, longest chunk of all
-// Waves of their own for the outputs while the workgroups have places: a workgroup of d_k 64 has half
-// the waves.  The wide one where it has more workgroups than places.
+// Which scan, by the number of slices of 16 columns (bf16, 32 heads, uneven lengths up to 2048; us with
+// what rule_prepare takes before it):
+//   d_k 128, slices           512    768   1024   2048   3072   4096
+//   outputs by own waves      134    116    209    334    720    703   narrowest, shortest chunk of all
+//   two column blocks         135    123    182    256    520    499   half the operands read per column
+//   wide                      203    189    219    290    473    442   a quarter, longest chunk of all
+//   d_k 64, slices            512   1024   1536   2048   3072   4096
+//   outputs by own waves      117    162    361    337    503    674
+//   two column blocks         160    189    327    291    425    580
+//   wide                      166    185    305    290    370    522
+// Waves of their own for the outputs while the workgroups have places (a workgroup of d_k 64 has half
+// the waves); half as many again would still be no loss at d_k 128.  The wide one where it has more
+// workgroups than places.  Slices alone decide, lengths do not: a sequence of many rows among
+// enough short ones takes the wide scan, 5 us a chunk, where the narrow one takes 1.9.
 template <int DK>
 constexpr int64_t kFewSlices = kPlaces * 128 / DK;
 template <int IO, int DK>
@@ -1693,8 +1700,8 @@ hipError_t rule_forward_launch(const RuleArgs& args, hipStream_t stream) {
     hipError_t e = hipSuccess;
     const bool wide = IO == GDN_BF16 && DK <= 128 && slices_of_16(a) > 4 * kPlaces;
     // The wide scan takes keys and queries from their rows where these are whole operands, 16 bytes at a time,
-    // and 64 of them within a lane's 32-bit offset (25331 rows, 16 heads of 128: 608 us for
-    // both kernels, 623 through prepared operands, which are 210 MB more to write).
+    // and 64 of them within a lane's 32-bit offset (25331 rows, 16 heads of 128: 646 us for
+    // both kernels, 670 through prepared operands, which are 210 MB more to write).
     constexpr int64_t kNear = 1 << 24;
     a.direct = wide && a.dk == DK && a.vk && a.vq && a.k.row <= kNear && a.q.row <= kNear;
     if (a.T > 0)
@@ -1730,6 +1737,8 @@ hipError_t back_launch(const RuleArgs& a, hipStream_t stream) {
     return e;
 }
 
+// One column block to a workgroup while they have places.  Both scans, one block against two, bf16, 32 heads, us:
+// d_k 128, 512 slices 289 and 306, 768 slices 398 and 355; d_k 64, 512 slices 249 and 263, 768 slices 353 and 317.
 template <int IO, int DK>
 hipError_t rule_backward_launch(const RuleArgs& a, hipStream_t stream) {
     if constexpr (DK == 256)

@@ -4,8 +4,8 @@
 // One pass over a row keeps, per thread, the running maximum m and, with d = (x - m) log2 e, s = sum
 // 2^d and t = sum 2^d d; a change of m by d turns them into 2^d s and 2^d (t + d s).  Then lse = m +
 // ln s and the entropy is ln s - (t / s) ln 2.  Both kernels are bound by the logits' bytes; the
-// exponentials and sums take two thirds of that time.  8192 rows of 65536, bf16: 202 us, 5.3 TB/s read;
-// the gradient of 4096 such rows: 194 us, 5.5 TB/s read and written.
+// exponentials and sums take two thirds of that time.  8192 rows of 65536, bf16: 205 us, 5.2 TB/s read;
+// the gradient of 4096 such rows: 195 us, 5.5 TB/s read and written.
 //
 // The best alternative is in the piece of 16 bytes where its thread last raised its maximum.  More
 // alternatives come of a bound that at least k of the threads' maxima reach: the least maximum of
