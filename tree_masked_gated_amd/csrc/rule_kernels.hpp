@@ -1680,14 +1680,14 @@ hipError_t scan_launch(const RuleArgs& a, hipStream_t stream) {
 
 // Which scan, by the number of slices of 16 columns (bf16, 32 heads, uneven lengths up to 2048; us with
 // what rule_prepare takes before it):
-//   d_k 128, slices           512    768   1024   2048   3072   4096
-//   outputs by own waves      134    116    209    334    720    703   narrowest, shortest chunk of all
-//   two column blocks         135    123    182    256    520    499   half the operands read per column
-//   wide                      203    189    219    290    473    442   a quarter, longest chunk of all
-//   d_k 64, slices            512   1024   1536   2048   3072   4096
-//   outputs by own waves      117    162    361    337    503    674
-//   two column blocks         160    189    327    291    425    580
-//   wide                      166    185    305    290    370    522
+//   d_k 128, slices           512    768   1024   2048   4096
+//   outputs by own waves      134    116    209    334    703   narrowest, shortest chunk of all
+//   two column blocks         135    123    182    256    499   half the operands read per column
+//   wide                      203    189    219    290    442   a quarter, longest chunk of all
+//   d_k 64, slices            512   1024   1536   2048   4096
+//   outputs by own waves      117    162    361    337    674
+//   two column blocks         160    189    327    291    580
+//   wide                      166    185    305    290    522
 // Waves of their own for the outputs while the workgroups have places (a workgroup of d_k 64 has half
 // the waves); half as many again would still be no loss at d_k 128.  The wide one where it has more
 // workgroups than places.  Slices alone decide, lengths do not: a sequence of many rows among
