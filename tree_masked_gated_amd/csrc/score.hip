@@ -258,8 +258,10 @@ __global__ void __launch_bounds__(NT) score_rows(const ScoreArgs a) {
     if (topk > 0) {
         if (topk == 1) low = high;
         // past eight groups their least maximum is far below the k-th of all: low's reach, at least
-        // topk threads, is halved until few more are left
-        if (topk > 8)
+        // topk threads, is halved until few more are left; so it is where a group has no elements at
+        // all, and its maximum lets every element through (8192 rows of 540 to 2000, 8 alternatives, bf16: 115
+        // us, where ordering all elements took 940)
+        if (topk > 8 || (topk > 1 && sp.pieces <= NT - 64))
             for (int step = 0; step < 20 && high - low > 1; ++step) {
                 const uint32_t mid = low + (high - low) / 2;
                 const int have = __popcll(__ballot(mine >= mid));
